@@ -116,7 +116,7 @@ def prepare(case, seed):
             s["av"] = av
             s["lin"] = av.QuantLinear(s["wq"], s["ws"], K, s["bias"])
             if case["op"] == "score":
-                s["work"] = av.score_workspace(T, N, DEV)
+                s["work"] = av.score_workspace(T, s["lin"])
         return s
     V = case["V"]
     # a masked token: most words unlikely, a few far ahead
