@@ -13,12 +13,16 @@ Entry points (same names as the C ABI):
   avey_compress      eq. 8 neural compression with residual
   avey_dynamic_mix   eq. 6 row-normalised cosine mix of split blocks
   avey_layer_forward enricher -> static/dynamic mix -> fuser + residual
+  avey_linear_i8     8-bit product with a scale per token and channel
+  avey_token_logprobs log probabilities, entropy and top alternatives of logits
+  avey_score_tokens_i8 the 8-bit product with a vocabulary matrix, scored
 and ``encoder_forward`` which strings them together (ranker once, then every
 layer), the call a user of the encoder makes; ``processor_forward`` is the
 same forward after the ranker, for a selection the caller supplies.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -29,9 +33,10 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libavey.so")
 
-AVEY_F32, AVEY_BF16, AVEY_BF16X2 = 0, 1, 2
+AVEY_F32, AVEY_BF16, AVEY_BF16X2, AVEY_I8 = 0, 1, 2, 3
 AVEY_STATIC, AVEY_DYNAMIC, AVEY_COUPLED_CAUSAL = 0, 1, 2
 AVEY_RANK_UNIDIRECTIONAL = 1
+AVEY_ACT_NONE, AVEY_ACT_RELU2 = 0, 1
 STATUS = {0: "AVEY_OK", 1: "AVEY_ERR_INVALID_ARG", 2: "AVEY_ERR_UNSUPPORTED", 3: "AVEY_ERR_CUDA",
           4: "AVEY_ERR_DEVICE_TIMEOUT", 5: "AVEY_ERR_DEVICE_BOUNDS"}
 
@@ -51,6 +56,11 @@ class AveyError(RuntimeError):
 class LayerParams(ctypes.Structure):
     _fields_ = [("kind", _i), ("d", _i), ("m", _i), ("m_h", _i), ("S", _i), ("eps", ctypes.c_float),
                 ("prenorm", _i), ("Ut", _vp), ("bU", _vp), ("V", _vp), ("Ot", _vp)]
+
+
+class LinearI8Params(ctypes.Structure):
+    _fields_ = [("K", _i), ("N", _i), ("Wq", _vp), ("ld_w", _i64), ("w_scale", _vp), ("bias", _vp),
+                ("act", _i)]
 
 
 def lib() -> ctypes.CDLL:
@@ -103,6 +113,23 @@ def lib() -> ctypes.CDLL:
         L.avey_compress_rows.argtypes = [_vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp,
                                          _vp, _vp]
         L.avey_compress_rows.restype = _i
+        L.avey_quantize_rows.argtypes = [_vp, _i, _i, _i, _i64, _i, _vp, _i64, _vp, _vp]
+        L.avey_quantize_rows.restype = _i
+        L.avey_linear_i8.argtypes = [ctypes.POINTER(LinearI8Params), _vp, _i, _i64, _vp, _i, _i, _vp, _vp,
+                                     _i, _i64, _vp, _sz, _vp]
+        L.avey_linear_i8.restype = _i
+        L.avey_linear_i8_workspace_bytes.argtypes = [_i, _i, _i]
+        L.avey_linear_i8_workspace_bytes.restype = _sz
+        L.avey_token_logprobs.argtypes = [_vp, _i, _i, _i, _i64, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp]
+        L.avey_token_logprobs.restype = _i
+        L.avey_token_logprobs_backward.argtypes = [_vp, _i, _i, _i, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                                   _i64, _vp]
+        L.avey_token_logprobs_backward.restype = _i
+        L.avey_score_tokens_i8.argtypes = [ctypes.POINTER(LinearI8Params), _vp, _i, _i64, _vp, _i, _i, _vp,
+                                           _vp, _vp, _vp, _vp, _sz, _vp]
+        L.avey_score_tokens_i8.restype = _i
+        L.avey_score_tokens_i8_workspace_bytes.argtypes = [_i, _i, _i]
+        L.avey_score_tokens_i8_workspace_bytes.restype = _sz
         L.avey_device_status.argtypes = [_vp]
         L.avey_device_status.restype = _i
         L.avey_status_string.argtypes = [_i]
@@ -327,6 +354,267 @@ def avey_static_mix(V: torch.Tensor, zt: torch.Tensor, S: int, mt: Optional[int]
     return out
 
 
+# --------------------------------------------------- 8-bit products, scoring --
+
+_here = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor):
+    """Makes t's device current, so that the call runs on its current stream."""
+    return _here if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _same_device(t: torch.Tensor, *others) -> None:
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"tensors on {t.device} and {o.device} in one call")
+
+
+def _rows_of(t: torch.Tensor, name: str):
+    """(rows, cols, ld) of a CUDA matrix whose rows are contiguous."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA matrix")
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    if cols < 1 or (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous, non-overlapping rows of at least one column")
+    return rows, cols, ld
+
+
+def _vector(t: Optional[torch.Tensor], name: str, n: int, dtype: torch.dtype) -> None:
+    if t is None:
+        return
+    _need(t, name)
+    if t.dtype != dtype or t.shape != (n,):
+        raise TypeError(f"{name} must be {dtype} [{n}]")
+
+
+def _quant_source(x: torch.Tensor, name: str = "x"):
+    """(dtype code, rows, cols, ld) of activations to be quantised."""
+    if x.dim() == 3 and x.dtype == torch.bfloat16 and x.shape[0] == 2:
+        _need(x, name)
+        if x.shape[2] < 1:
+            raise ValueError(f"{name} must have at least one column")
+        return AVEY_BF16X2, x.shape[1], x.shape[2], x.shape[2]
+    rows, cols, ld = _rows_of(x, name)
+    return _dt(x), rows, cols, ld
+
+
+@dataclass
+class QuantRows:
+    """Rows as 8-bit integers: row t stands for scale[t] * q[t, :cols]."""
+    q: torch.Tensor  # int8 [rows, ld], ld a multiple of 16
+    scale: torch.Tensor  # fp32 [rows]
+    cols: int
+
+
+@dataclass
+class QuantLinear:
+    """Weights of an 8-bit product: channel n is scale[n] * q[n, :K]."""
+    q: torch.Tensor  # int8 [N, ld], ld a multiple of 16
+    scale: torch.Tensor  # fp32 [N]
+    K: int
+    bias: Optional[torch.Tensor] = None  # fp32 [N]
+
+    def __post_init__(self):
+        N = self.q.shape[0] if self.q.dim() == 2 else -1
+        if not (self.q.is_cuda and self.q.dtype == torch.int8 and N >= 1 and self.q.is_contiguous()
+                and self.q.shape[1] % 16 == 0 and 1 <= self.K <= self.q.shape[1]):
+            raise ValueError("q must be a contiguous CUDA int8 [N, ld] with ld % 16 == 0 and K <= ld")
+        _vector(self.scale, "scale", N, torch.float32)
+        _vector(self.bias, "bias", N, torch.float32)
+        _same_device(self.q, self.scale, self.bias)
+
+    def _params(self, act: int) -> LinearI8Params:
+        return LinearI8Params(self.K, self.q.shape[0], self.q.data_ptr(), self.q.shape[1],
+                              self.scale.data_ptr(), None if self.bias is None else self.bias.data_ptr(),
+                              act)
+
+
+def avey_quantize_rows(x: torch.Tensor, prenorm: bool = False) -> QuantRows:
+    """Rows of x (fp32 or bf16 [rows, cols], any row stride, or a split pair
+    [2, rows, cols]) as 8-bit integers with a scale per row; prenorm: of the
+    RMS-normalised rows."""
+    dt, rows, cols, ld = _quant_source(x)
+    q = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=x.device)
+    scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    with _on(x):
+        _check("avey_quantize_rows", lib().avey_quantize_rows(
+            _ptr(x), dt, rows, cols, ld, int(bool(prenorm)), _ptr(q), q.shape[1], _ptr(scale), _stream()))
+    return QuantRows(q, scale, cols)
+
+
+def quantize_linear(W: torch.Tensor, bias: Optional[torch.Tensor] = None) -> QuantLinear:
+    """Weights [N, K] (fp32 or bf16) with a scale for each output channel."""
+    r = avey_quantize_rows(W)
+    return QuantLinear(r.q, r.scale, r.cols, bias)
+
+
+def _linear_input(x, lin: QuantLinear):
+    """(tensor, dtype code, rows, ld, scale) of a product's input."""
+    if isinstance(x, QuantRows):
+        _need(x.q, "x.q")
+        if x.q.dtype != torch.int8 or x.q.dim() != 2 or x.q.shape[1] < x.cols:
+            raise TypeError("x.q must be int8 [rows, ld] with ld >= cols")
+        _vector(x.scale, "x.scale", x.q.shape[0], torch.float32)
+        t, dt, rows, cols, ld, scale = x.q, AVEY_I8, x.q.shape[0], x.cols, x.q.shape[1], x.scale
+    else:
+        dt, rows, cols, ld = _quant_source(x)
+        t, scale = x, None
+    if cols != lin.K:
+        raise ValueError(f"x has {cols} columns, the weights {lin.K}")
+    _same_device(t, scale, lin.q)
+    return t, dt, rows, ld, scale
+
+
+def avey_linear_i8(x, lin: QuantLinear, act: int = AVEY_ACT_NONE,
+                   residual: Optional[torch.Tensor] = None, prenorm: bool = False,
+                   out_dtype: torch.dtype = torch.float32, pair: bool = False,
+                   out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """act(x W^T + bias) + residual in 8-bit integers.
+
+    x: QuantRows, or activations quantised within the call (fp32 or bf16
+    [rows, K], or a split pair [2, rows, K]).  residual: fp32 [rows, N].
+    Returns [rows, N] of out_dtype (fp32 or bf16), or with pair=True the bf16
+    split pair [2, rows, N]; rows are padded to a multiple of 8 values, so for
+    other N the result is a view.  ``out`` (fp32, bf16 or, with pair, the pair;
+    row stride a multiple of 8) is written instead when given; it may be the
+    residual.
+    """
+    t, dt, rows, ld, scale = _linear_input(x, lin)
+    N = lin.q.shape[0]
+    if out is None:
+        ld_out = (N + 7) // 8 * 8
+        shape = (2, rows, ld_out) if pair else (rows, ld_out)
+        out = torch.empty(shape, dtype=torch.bfloat16 if pair else out_dtype, device=t.device)
+        if ld_out != N:
+            out = out[..., :N]
+    elif pair:
+        _need(out, "out")
+        if out.dtype != torch.bfloat16 or out.shape != (2, rows, N):
+            raise TypeError(f"out must be a bf16 pair [2, {rows}, {N}]")
+        ld_out = N
+    else:
+        r, c, ld_out = _rows_of(out, "out")
+        if (r, c) != (rows, N):
+            raise TypeError(f"out must be [{rows}, {N}]")
+        if rows <= 1:
+            ld_out = (N + 7) // 8 * 8
+    out_dt = AVEY_BF16X2 if pair else _dt(out)
+    if residual is not None:
+        r, c, ld_r = _rows_of(residual, "residual")
+        if residual.dtype != torch.float32 or (r, c) != (rows, N):
+            raise TypeError(f"residual must be fp32 [{rows}, {N}]")
+        if (rows > 1 and ld_r != ld_out) or residual.data_ptr() % 16:
+            padded = torch.empty((rows, ld_out), dtype=torch.float32, device=t.device)
+            padded[:, :N].copy_(residual)
+            residual = padded
+    _same_device(t, out, residual, ws)
+    L = lib()
+    with _on(t):
+        need = 0 if dt == AVEY_I8 else int(L.avey_linear_i8_workspace_bytes(dt, rows, lin.K))
+        if need and (ws is None or ws.numel() < need):
+            ws = _ws(need, t.device)
+        p = lin._params(act)
+        _check("avey_linear_i8", L.avey_linear_i8(
+            ctypes.byref(p), _ptr(t), dt, ld, _ptr(scale), int(bool(prenorm)), rows, _ptr(residual),
+            _ptr(out), out_dt, ld_out, _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
+    return out
+
+
+@dataclass
+class TokenLogprobs:
+    """Scores of logits rows; lse = stats.sum(1) is the log of the sum of exponentials."""
+    logprob: Optional[torch.Tensor]  # fp32 [rows], of the given tokens
+    stats: torch.Tensor  # fp32 [rows, 2]: maximum, log of the sum relative to it
+    entropy: torch.Tensor  # fp32 [rows]
+    top_ids: Optional[torch.Tensor] = None  # int32 [rows, top]
+    top_logprobs: Optional[torch.Tensor] = None  # fp32 [rows, top]
+
+
+def avey_token_logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None,
+                        top: int = 0) -> TokenLogprobs:
+    """Log probabilities of ids (int32 [rows], negative: none) under logits
+    (fp32 or bf16 [rows, V], any row stride), entropies and the ``top`` words.
+
+    No autograd graph is recorded: avey_token_logprobs_backward gives the
+    gradient of the logits.
+    """
+    rows, V, ld = _rows_of(logits, "logits")
+    dt = _dt(logits)
+    _vector(ids, "ids", rows, torch.int32)
+    _same_device(logits, ids)
+    f = lambda *s: torch.empty(s, dtype=torch.float32, device=logits.device)
+    logprob = None if ids is None else f(rows)
+    stats, entropy = f(rows, 2), f(rows)
+    top_ids = top_lp = None
+    if top > 0:
+        top_ids, top_lp = torch.empty((rows, top), dtype=torch.int32, device=logits.device), f(rows, top)
+    with _on(logits):
+        _check("avey_token_logprobs", lib().avey_token_logprobs(
+            _ptr(logits), dt, rows, V, ld, _ptr(ids), top, _ptr(logprob), _ptr(stats), _ptr(entropy),
+            _ptr(top_ids), _ptr(top_lp), _stream()))
+    return TokenLogprobs(logprob, stats, entropy, top_ids, top_lp)
+
+
+def avey_token_logprobs_backward(logits: torch.Tensor, ids: Optional[torch.Tensor], scores: TokenLogprobs,
+                                 d_logprob: Optional[torch.Tensor],
+                                 d_entropy: Optional[torch.Tensor] = None,
+                                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of sum(d_logprob * logprob) + sum(d_entropy * entropy) with
+    respect to the logits; scores: what avey_token_logprobs gave for them.
+    out may be the logits."""
+    rows, V, ld = _rows_of(logits, "logits")
+    dt = _dt(logits)
+    _vector(ids, "ids", rows, torch.int32)
+    _vector(d_logprob, "d_logprob", rows, torch.float32)
+    _vector(d_entropy, "d_entropy", rows, torch.float32)
+    _vector(scores.entropy, "entropy", rows, torch.float32)
+    _need(scores.stats, "stats")
+    if scores.stats.dtype != torch.float32 or scores.stats.shape != (rows, 2):
+        raise TypeError(f"stats must be fp32 [{rows}, 2]")
+    if out is None:
+        out = torch.empty((rows, V), dtype=logits.dtype, device=logits.device)
+    r, c, ld_d = _rows_of(out, "out")
+    if (r, c) != (rows, V) or out.dtype != logits.dtype:
+        raise TypeError(f"out must be {logits.dtype} [{rows}, {V}]")
+    _same_device(logits, ids, scores.stats, scores.entropy, d_logprob, d_entropy, out)
+    with _on(logits):
+        _check("avey_token_logprobs_backward", lib().avey_token_logprobs_backward(
+            _ptr(logits), dt, rows, V, ld, _ptr(ids), _ptr(scores.stats), _ptr(scores.entropy),
+            _ptr(d_logprob), _ptr(d_entropy), _ptr(out), ld_d, _stream()))
+    return out
+
+
+def score_workspace(rows: int, head: QuantLinear) -> torch.Tensor:
+    """Workspace of avey_score_tokens_i8 for up to ``rows`` rows."""
+    n = lib().avey_score_tokens_i8_workspace_bytes(rows, head.K, head.q.shape[0])
+    return _ws(n, head.q.device)
+
+
+def avey_score_tokens_i8(x, head: QuantLinear, ids: Optional[torch.Tensor] = None, prenorm: bool = False,
+                         ws: Optional[torch.Tensor] = None) -> TokenLogprobs:
+    """Log probabilities of ids (int32 [rows], negative: none) and entropies
+    under the vocabulary head, from hidden states x (as avey_linear_i8's);
+    the logits are not an output."""
+    t, dt, rows, ld, scale = _linear_input(x, head)
+    _vector(ids, "ids", rows, torch.int32)
+    _same_device(t, ids, ws)
+    f = lambda *s: torch.empty(s, dtype=torch.float32, device=t.device)
+    logprob = None if ids is None else f(rows)
+    stats, entropy = f(rows, 2), f(rows)
+    L = lib()
+    with _on(t):
+        need = int(L.avey_score_tokens_i8_workspace_bytes(rows, head.K, head.q.shape[0]))
+        if need and (ws is None or ws.numel() < need):
+            ws = _ws(need, t.device)
+        p = head._params(AVEY_ACT_NONE)
+        _check("avey_score_tokens_i8", L.avey_score_tokens_i8(
+            ctypes.byref(p), _ptr(t), dt, ld, _ptr(scale), int(bool(prenorm)), rows, _ptr(ids),
+            _ptr(logprob), _ptr(stats), _ptr(entropy), _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
+    return TokenLogprobs(logprob, stats, entropy)
+
+
 # ------------------------------------------------------------------ layer --
 
 @dataclass
@@ -412,6 +700,49 @@ def device_layers(weights, dtype: torch.dtype, device) -> List[DeviceLayer]:
 
 
 @dataclass
+class QuantLayer:
+    """One layer with its enricher and fuser as 8-bit products; the mix between
+    them stays on the bf16 split pair."""
+    kind: int  # AVEY_STATIC or AVEY_DYNAMIC
+    U: QuantLinear  # [m, d], bias bU
+    V: Optional[torch.Tensor]  # [S, S] bf16 or None
+    O: QuantLinear  # [d, m]
+
+
+def quantize_layers(layers: Sequence[DeviceLayer]) -> List[QuantLayer]:
+    """The layers with 8-bit weights, for encoder_forward and the other
+    forwards with compression (bf16 embeddings, static and dynamic layers)."""
+    out = []
+    for lay in layers:
+        if lay.kind not in (AVEY_STATIC, AVEY_DYNAMIC):
+            raise ValueError("8-bit layers are static or dynamic")
+        V = None if lay.V is None else lay.V.to(torch.bfloat16).contiguous()
+        out.append(QuantLayer(lay.kind, quantize_linear(lay.Ut, lay.bU), V, quantize_linear(lay.Ot)))
+    return out
+
+
+def _quantized(layers) -> bool:
+    """Whether the layers are 8-bit ones (all of them or none)."""
+    n = sum(isinstance(lay, QuantLayer) for lay in layers)
+    if n not in (0, len(layers)):
+        raise TypeError("a stack is made of DeviceLayer or of QuantLayer, not both")
+    return n > 0
+
+
+def _inner_width(layers, d: int) -> int:
+    """m, the enricher's output width."""
+    if not layers:
+        return d
+    return layers[0].U.q.shape[0] if _quantized(layers) else layers[0].Ut.shape[0]
+
+
+def layer_i8_workspace_bytes(T: int, d: int, m: int) -> int:
+    """Z as a split pair, and the 8-bit rows of x or of Z."""
+    L = lib()
+    return T * m * 4 + 256 + max(int(L.avey_linear_i8_workspace_bytes(AVEY_F32, T, k)) for k in (d, m))
+
+
+@dataclass
 class EncoderWorkspace:
     """Preallocated buffers for encoder_forward at one shape (reused per call)."""
     rank_ws: torch.Tensor
@@ -427,15 +758,17 @@ class EncoderWorkspace:
 
 
 def make_workspace(B: int, N: int, d: int, S: int, k: int, m: int, dtype: torch.dtype, prenorm: bool,
-                   device, uncompressed: bool = False) -> EncoderWorkspace:
+                   device, uncompressed: bool = False, quantized: bool = False) -> EncoderWorkspace:
     """Buffers for encoder_forward, or (uncompressed=True) for
-    encoder_forward_uncompressed, whose layers run on B*n*(k+1)S tokens."""
+    encoder_forward_uncompressed, whose layers run on B*n*(k+1)S tokens;
+    quantized=True: for 8-bit layers too (else they allocate their scratch)."""
     n = -(-N // S)
     blk = (k + 1) * S if uncompressed else S
     T = B * n * blk
     dt = AVEY_BF16 if dtype == torch.bfloat16 else AVEY_F32
     rank_ws = _ws(rank_workspace_bytes(dt, B, N, d, S), device)
-    layer_ws = _ws(layer_workspace_bytes(dt, T, d, m, prenorm, blk, AVEY_DYNAMIC), device)
+    need = layer_workspace_bytes(dt, T, d, m, prenorm, blk, AVEY_DYNAMIC)
+    layer_ws = _ws(max(need, layer_i8_workspace_bytes(T, d, m)) if quantized else need, device)
     idx = torch.empty((B, n, k), dtype=torch.int32, device=device)
     w = torch.empty((B, n, k), dtype=torch.float32, device=device)
     x0 = torch.empty((T, d), dtype=torch.float32, device=device)
@@ -453,14 +786,58 @@ def make_workspace(B: int, N: int, d: int, S: int, k: int, m: int, dtype: torch.
 
 def _pair_stream(dt: int, layers) -> bool:
     """bf16 stacks pass the residual stream between the calls as its split pair
-    alone; fp32 is written once, by the last layer."""
-    return dt == AVEY_BF16 and len(layers) > 0
+    alone; fp32 is written once, by the last layer.  8-bit stacks keep it fp32."""
+    return dt == AVEY_BF16 and len(layers) > 0 and not _quantized(layers)
+
+
+def _run_layers_i8(L, layers, dt, T, d, m, m_h, S, eps, prenorm, ws, st, marks):
+    """Every 8-bit layer over the fp32 stream in ws.x0; returns the output
+    buffer.  Per layer: the enricher product (quantising its input) to the
+    split pair Z, the mix in place on Z's tail, the fuser product with the
+    residual."""
+    if dt != AVEY_BF16:
+        raise TypeError("8-bit layers take bf16 embeddings")
+    if m_h % 8 or not 0 < m_h < m:
+        raise ValueError(f"need 0 < m_h < m = {m}, m_h a multiple of 8 (m_h = {m_h})")
+    for lay in layers:
+        if (lay.U.K, lay.U.q.shape[0], lay.O.K, lay.O.q.shape[0]) != (d, m, m, d):
+            raise ValueError(f"8-bit layer products must be [{m}, {d}] and [{d}, {m}]")
+        if lay.kind == AVEY_STATIC and (lay.V is None or tuple(lay.V.shape) != (S, S)):
+            raise ValueError(f"a static layer needs V [{S}, {S}]")
+        _same_device(ws.x0, lay.U.q, lay.O.q, lay.V)
+    need = layer_i8_workspace_bytes(T, d, m)
+    lws = ws.layer_ws if ws.layer_ws.numel() >= need else _ws(need, ws.x0.device)
+    z = lws.data_ptr()
+    q = (z + T * m * 4 + 255) // 256 * 256
+    q_bytes = z + lws.numel() - q
+    cur, nxt = ws.x0, ws.x1
+    for li, lay in enumerate(layers):
+        pu, po = lay.U._params(AVEY_ACT_RELU2), lay.O._params(AVEY_ACT_NONE)
+        _check("avey_linear_i8", L.avey_linear_i8(
+            ctypes.byref(pu), _ptr(cur), AVEY_F32, d, None, int(bool(prenorm)), T, None, z, AVEY_BF16X2, m,
+            q, q_bytes, st))
+        tail = ctypes.c_void_p(z + 2 * m_h)
+        if lay.kind == AVEY_STATIC:
+            _check("avey_static_mix", L.avey_static_mix(_ptr(lay.V), tail, m, AVEY_BF16X2, T // S, S, m - m_h,
+                                                        tail, m, st))
+        else:
+            _check("avey_dynamic_mix", L.avey_dynamic_mix(tail, m, AVEY_BF16X2, T // S, S, m - m_h, eps, tail,
+                                                          m, st))
+        _check("avey_linear_i8", L.avey_linear_i8(
+            ctypes.byref(po), z, AVEY_BF16X2, m, None, 0, T, _ptr(cur), _ptr(nxt), AVEY_F32, d, q, q_bytes,
+            st))
+        if marks is not None:
+            marks[3 + li].record()
+        cur, nxt = nxt, cur
+    return cur
 
 
 def _run_layers(L, layers, dt, T, d, m, m_h, S, eps, prenorm, ws, st, marks):
     """Every layer over the stream in (ws.x0, ws.pair0); returns the fp32 output
     buffer.  ``marks[3 + li]`` is recorded after layer li.  With prenorm, each
     layer but the last also writes its output's row scales for the next one."""
+    if _quantized(layers):
+        return _run_layers_i8(L, layers, dt, T, d, m, m_h, S, eps, prenorm, ws, st, marks)
     pair_only = _pair_stream(dt, layers)
     hand_rms = bool(prenorm) and ws.rms0 is not None
     cur, nxt = (ws.x0, ws.pair0, ws.rms0), (ws.x1, ws.pair1, ws.rms1)
@@ -484,20 +861,21 @@ def _run_layers(L, layers, dt, T, d, m, m_h, S, eps, prenorm, ws, st, marks):
     return cur[0]
 
 
-def encoder_forward(x: torch.Tensor, P: torch.Tensor, layers: Sequence[DeviceLayer], S: int, k: int,
+def encoder_forward(x: torch.Tensor, P: torch.Tensor, layers: Sequence, S: int, k: int,
                     m_h: int, eps: float, prenorm: bool,
                     ws: Optional[EncoderWorkspace] = None, marks=None,
                     causal: bool = False) -> torch.Tensor:
     """Ranker once, compression, then every layer (Avey-B paperlayer summary
     App. H: the ranker runs once per forward).  Returns fp32 [B, n*S, d].
+    layers: DeviceLayer, or QuantLayer (quantize_layers) for 8-bit products.
 
     ``marks``: optional list of 3 + len(layers) torch.cuda.Event, recorded on
     the current stream before the ranker and after every C-ABI call.
     """
     B, N, d = x.shape
-    m = layers[0].Ut.shape[0] if layers else d
+    m = _inner_width(layers, d)
     if ws is None:
-        ws = make_workspace(B, N, d, S, k, m, x.dtype, prenorm, x.device)
+        ws = make_workspace(B, N, d, S, k, m, x.dtype, prenorm, x.device, quantized=_quantized(layers))
     dt = _dt(x)
     L = lib()
     st = _stream()
@@ -525,9 +903,9 @@ def processor_forward(x: torch.Tensor, P: torch.Tensor, layers: Sequence[DeviceL
     n = -(-N // S)
     T = B * n * S
     dt = _dt(x)
-    m = layers[0].Ut.shape[0] if layers else d
+    m = _inner_width(layers, d)
     if ws is None:
-        ws = make_workspace(B, N, d, S, k, m, x.dtype, prenorm, x.device)
+        ws = make_workspace(B, N, d, S, k, m, x.dtype, prenorm, x.device, quantized=_quantized(layers))
     for t, nm in ((idx, "idx"), (w, "w")):
         _need(t, nm)
         if t.numel() != B * n * k:
@@ -538,7 +916,7 @@ def processor_forward(x: torch.Tensor, P: torch.Tensor, layers: Sequence[DeviceL
     st = _stream()
     _check("avey_compress", L.avey_compress(_ptr(x), dt, B, N, d, S, k, _ptr(idx), _ptr(w),
                                             _ptr(P), None if _pair_stream(dt, layers) else _ptr(ws.x0),
-                                            _ptr(ws.pair0), st))
+                                            None if _quantized(layers) else _ptr(ws.pair0), st))
     if marks is not None:
         marks[2].record()
     out = _run_layers(L, layers, dt, T, d, m, m_h, S, eps, prenorm, ws, st, marks)
@@ -558,8 +936,10 @@ def encoder_forward_uncompressed(x: torch.Tensor, layers: Sequence[DeviceLayer],
     ``marks``: optional list of 3 + len(layers) torch.cuda.Event, recorded on
     the current stream before the ranker and after every C-ABI call.
     """
+    if _quantized(layers):
+        raise TypeError("8-bit layers run with compression only")
     B, N, d = x.shape
-    m = layers[0].Ut.shape[0] if layers else d
+    m = _inner_width(layers, d)
     if ws is None:
         ws = make_workspace(B, N, d, S, k, m, x.dtype, prenorm, x.device, uncompressed=True)
     dt = _dt(x)
@@ -583,12 +963,14 @@ def processor_forward_uncompressed(x: torch.Tensor, layers: Sequence[DeviceLayer
     """The uncompressed processor for a given selection (idx int32 [B, n, k],
     w fp32 [B, n, k]): every split's context through every layer.  Returns
     fp32 [B, n, S, d] (a view); ``marks`` as in processor_forward."""
+    if _quantized(layers):
+        raise TypeError("8-bit layers run with compression only")
     B, N, d = x.shape
     n = -(-N // S)
     L_ = (k + 1) * S
     T = B * n * L_
     dt = _dt(x)
-    m = layers[0].Ut.shape[0] if layers else d
+    m = _inner_width(layers, d)
     if ws is None:
         ws = make_workspace(B, N, d, S, k, m, x.dtype, prenorm, x.device, uncompressed=True)
     for t, nm in ((idx, "idx"), (w, "w")):
@@ -705,7 +1087,7 @@ def encoder_forward_sharded(x: torch.Tensor, P: torch.Tensor, layers: Sequence[D
     if dt != AVEY_BF16:
         raise TypeError("the sharded forward takes bf16 embeddings")
     n = -(-N // S)
-    m = layers[0].Ut.shape[0] if layers else d
+    m = _inner_width(layers, d)
     if ws is None:
         ws = make_shard_workspace(B, N, d, S, k, m, x.dtype, prenorm, rank, world, x.device)
     L = lib()
@@ -728,7 +1110,8 @@ def encoder_forward_sharded(x: torch.Tensor, P: torch.Tensor, layers: Sequence[D
                                               _ptr(ws.w), st))
     _check("avey_compress_rows", L.avey_compress_rows(
         _ptr(x), dt, B, N, d, S, k, t0, t1, _ptr(ws.idx), _ptr(ws.w), _ptr(P),
-        None if _pair_stream(dt, layers) else _ptr(ws.x0), _ptr(ws.pair0), st))
+        None if _pair_stream(dt, layers) else _ptr(ws.x0),
+        None if _quantized(layers) else _ptr(ws.pair0), st))
     if marks is not None:
         marks[2].record()
     out = _run_layers(L, layers, dt, T, d, m, m_h, S, eps, prenorm, ws, st, marks)

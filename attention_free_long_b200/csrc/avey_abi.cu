@@ -113,9 +113,10 @@ int sm_count() {
   return g_sms[dev];
 }
 
-bool encode_map(CUtensorMap *map, bool fp32, const void *base, uint64_t inner, uint64_t rows,
-                uint64_t batch, uint64_t row_stride_bytes, uint64_t batch_stride_bytes,
-                uint32_t box_inner, uint32_t box_rows, int swizzle_bytes) {
+static bool encode_typed(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t inner,
+                         uint64_t rows, uint64_t batch, uint64_t row_stride_bytes,
+                         uint64_t batch_stride_bytes, uint32_t box_inner, uint32_t box_rows,
+                         int swizzle_bytes) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) {
     set_detail("cuTensorMapEncodeTiled is not available from the driver");
@@ -128,7 +129,7 @@ bool encode_map(CUtensorMap *map, bool fp32, const void *base, uint64_t inner, u
   const CUtensorMapSwizzle sw = swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                 : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                       : CU_TENSOR_MAP_SWIZZLE_NONE;
-  CUresult r = fn(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+  CUresult r = fn(map, type, 3,
                   const_cast<void *>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -139,6 +140,20 @@ bool encode_map(CUtensorMap *map, bool fp32, const void *base, uint64_t inner, u
     return false;
   }
   return true;
+}
+
+bool encode_map(CUtensorMap *map, bool fp32, const void *base, uint64_t inner, uint64_t rows,
+                uint64_t batch, uint64_t row_stride_bytes, uint64_t batch_stride_bytes,
+                uint32_t box_inner, uint32_t box_rows, int swizzle_bytes) {
+  return encode_typed(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      base, inner, rows, batch, row_stride_bytes, batch_stride_bytes, box_inner,
+                      box_rows, swizzle_bytes);
+}
+
+bool encode_i8_map(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
+                   uint64_t row_stride_bytes, uint32_t box_rows) {
+  return encode_typed(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, inner, rows, 1, row_stride_bytes,
+                      row_stride_bytes * rows, 128, box_rows, 128);
 }
 
 bool encode_bf16_map(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,

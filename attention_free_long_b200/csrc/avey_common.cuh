@@ -40,6 +40,10 @@ bool encode_bf16_map(CUtensorMap *map, const void *base, uint64_t inner, uint64_
 bool encode_map(CUtensorMap *map, bool fp32, const void *base, uint64_t inner, uint64_t rows,
                 uint64_t batch, uint64_t row_stride_bytes, uint64_t batch_stride_bytes,
                 uint32_t box_inner, uint32_t box_rows, int swizzle_bytes);
+// 8-bit 2-D map {inner, rows} as a 3-D map with batch 1, 128-byte swizzle, box
+// {128, box_rows, 1}.
+bool encode_i8_map(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
+                   uint64_t row_stride_bytes, uint32_t box_rows);
 
 #define AVEY_CHECK_LAUNCH(name, stream)                                     \
   do {                                                                      \
@@ -327,6 +331,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Instruction descriptor: s8 x s8 -> s32, both operands K-major.
+__host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
 // --- CTA pairs (clusters of 2) for cta_group::2 tensor-core tiles ---
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -377,6 +387,16 @@ __device__ __forceinline__ void tc_mma_bf16_pair(uint32_t tmem_d, uint64_t adesc
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same over 8-bit integers, int32 accumulators.
+__device__ __forceinline__ void tc_mma_i8_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }

@@ -109,4 +109,21 @@ avey_status launch_long_gram_tc(const bf16 *zhi, int64_t ldz, int blocks, int SL
 avey_status launch_long_mix_tc(const bf16 *a_hi, const bf16 *a_lo, bool a_batched, const bf16 *zhi,
                                const bf16 *zlo, int64_t ldz, int blocks, int SL, int mt, bf16 *chi,
                                bf16 *clo, cudaStream_t s);
+
+// ---- 8-bit products and token scoring ----
+// Checks of a source to be quantised (avey_quant.cu); fn names the entry point.
+avey_status check_quant_source(const char *fn, const void *x, avey_dtype dt, int cols, int64_t ld_x);
+avey_status launch_quantize_rows(const void *x, avey_dtype dt, int rows, int cols, int64_t ld_x,
+                                 int prenorm, int8_t *q, int64_t ld_q, float *scale, cudaStream_t s);
+// Checks of the arguments avey_linear_i8 and avey_score_tokens_i8 share
+// (avey_linear_i8.cu).
+avey_status check_linear_i8(const char *fn, const avey_linear_i8_params *p, const void *x,
+                            avey_dtype x_dt, int64_t ld_x, const float *x_scale, int prenorm, int rows);
+avey_status launch_linear_i8(const avey_linear_i8_params *p, const int8_t *xq, int64_t ld_xq,
+                             const float *x_scale, int rows, const float *residual, void *out,
+                             avey_dtype out_dt, int64_t ld_out, cudaStream_t s);
+// Arguments as avey_token_logprobs, checked by the caller (avey_logprobs.cu).
+avey_status launch_token_logprobs(const void *logits, avey_dtype dt, int rows, int V, int64_t ld,
+                                  const int32_t *ids, int top, float *logprob, float *stats,
+                                  float *entropy, int32_t *top_ids, float *top_lp, cudaStream_t s);
 }  // namespace avey

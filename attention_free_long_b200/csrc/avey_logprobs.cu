@@ -1,0 +1,631 @@
+// avey_logprobs.cu -- scoring of logits rows and its gradient.
+//
+//   m = max_j x_j, z = log sum_j exp(x_j - m), logprob = x_id - m - z,
+//   entropy = z - sum_j e_j (x_j - m) / sum_j e_j,  e_j = exp(x_j - m),
+//   the `top` largest by (value desc, index asc).
+//
+// Forward: one pass over the row with a running maximum; each thread carries
+// (m, s, t) = (max, sum e, sum e (x - m)) and rescales s and t once a batch
+// when its maximum grows.  A row belongs to one block, or to a cluster of up
+// to eight blocks when there are few rows, whose partial results meet in
+// distributed shared memory.
+// Alternatives: beside its maximum a thread keeps the vector it came from.
+// Every true alternative lies with one of the `top` threads of largest
+// (maximum, first vector): the vectors of different threads are disjoint
+// index ranges, so each of those threads holds an element that beats
+// everything of a thread behind them.  Only these threads' vectors (top / 256
+// of the row) are read a second time, an element below the last of those
+// maxima is dropped at once, and the rest goes through sorted 32-entry lists,
+// one a warp.
+// Backward: dx_j = g (1[j = id] - p_j) - h p_j (log p_j + entropy), one read and
+// one write of the row.
+#include <algorithm>
+#include <cmath>
+
+#include "avey_common.cuh"
+#include "avey_internal.h"
+
+namespace avey {
+namespace {
+
+constexpr int kLpThreads = 256, kLpWarps = 8;
+constexpr int kBatch = 4;             // 16-byte vectors a thread loads at once
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLowest = -3.402823466e38f;
+// exp(d) is 0 in fp32 from here down; keeps 0 * (x - m) finite
+constexpr float kFar = -200.0f;
+constexpr uint32_t kOrdNegInf = 0x007fffffu;
+
+__device__ __forceinline__ float fast_exp(float d) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * kLog2e));
+  return r;
+}
+
+// Unsigned integers in the order of the floats; -0 counts as +0.
+__device__ __forceinline__ uint32_t ord_of(float f) {
+  const uint32_t b = __float_as_uint(f + 0.0f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float ord_value(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+// (value desc, index asc) as one descending key; 0 is "none".
+__device__ __forceinline__ uint64_t key_of(float f, uint32_t index) {
+  return (static_cast<uint64_t>(ord_of(f)) << 32) | (~index);
+}
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(const uint4 &w, float *v) {
+    v[0] = __uint_as_float(w.x);
+    v[1] = __uint_as_float(w.y);
+    v[2] = __uint_as_float(w.z);
+    v[3] = __uint_as_float(w.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float *v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  }
+  static __device__ __forceinline__ float to_f(float x) { return x; }
+  static __device__ __forceinline__ float from_f(float x) { return x; }
+};
+template <>
+struct Vec<bf16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(const uint4 &w, float *v) {
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float *v) {
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                      pack_bf16(v[6], v[7]));
+  }
+  static __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ bf16 from_f(float x) { return __float2bfloat16_rn(x); }
+};
+
+// A row as 16-byte vectors of aligned addresses: vector u holds elements
+// u * N - shift .. , of which those outside [0, V) do not exist.
+template <typename T>
+struct Row {
+  static constexpr int N = Vec<T>::N;
+  const T *p;
+  int V, shift, vecs;
+  __device__ __forceinline__ Row(const T *base, int V_) : p(base), V(V_) {
+    shift = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(T));
+    vecs = static_cast<int>((static_cast<long long>(V) + shift + N - 1) / N);
+  }
+  __device__ __forceinline__ int first(int u) const { return u * N - shift; }
+  __device__ __forceinline__ bool whole(int u) const {
+    const int e = first(u);
+    return e >= 0 && e <= V - N;
+  }
+  __device__ __forceinline__ uint4 load_whole(int u) const {
+    return __ldg(reinterpret_cast<const uint4 *>(p + first(u)));
+  }
+  // elements that do not exist are -inf; plain loads, as the gradient may
+  // overwrite the row it reads
+  __device__ __forceinline__ void load_part(int u, float *v) const {
+    const int e = first(u);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      v[i] = (e + i >= 0 && e + i < V) ? Vec<T>::to_f(p[e + i]) : -INFINITY;
+  }
+  __device__ __forceinline__ void load(int u, float *v) const {
+    if (whole(u))
+      Vec<T>::unpack(*reinterpret_cast<const uint4 *>(p + first(u)), v);
+    else
+      load_part(u, v);
+  }
+};
+
+struct Stat {
+  float m, s, t;  // maximum (kLowest for none), sum e, sum e (x - m)
+};
+// s and t relative to M >= m
+__device__ __forceinline__ void rebase(Stat &a, float M) {
+  const float d = fmaxf(a.m - M, kFar), f = fast_exp(a.m - M);
+  a.t = f * fmaf(a.s, d, a.t);
+  a.s *= f;
+  a.m = M;
+}
+
+struct LpArgs {
+  const void *x;
+  long long ld;
+  int V, blocks;  // blocks of a row (the cluster size)
+  const int32_t *ids;
+  int top;
+  float *logprob, *stats, *entropy;
+  int32_t *top_ids;
+  float *top_lp;
+  int *status;
+};
+
+// Descending sort of one key per lane.
+__device__ __forceinline__ uint64_t warp_sort(uint64_t key, int lane) {
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1) {
+#pragma unroll
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      const uint64_t o = __shfl_xor_sync(0xffffffffu, key, j);
+      const bool first = ((lane & j) == 0) == ((lane & k) == 0);
+      key = (first == (key > o)) ? key : o;
+    }
+  }
+  return key;
+}
+// The 32 largest of two descending lists, descending.
+__device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b, int lane) {
+  const uint64_t r = __shfl_sync(0xffffffffu, b, 31 - lane);
+  uint64_t key = a > r ? a : r;
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) {
+    const uint64_t o = __shfl_xor_sync(0xffffffffu, key, j);
+    const bool first = (lane & j) == 0;
+    key = (first == (key > o)) ? key : o;
+  }
+  return key;
+}
+// The block's warps' descending lists into lists[0]; every thread calls it.
+__device__ __forceinline__ void block_merge(uint64_t (*lists)[32], int warp, int lane) {
+#pragma unroll
+  for (int h = kLpWarps / 2; h > 0; h >>= 1) {
+    __syncthreads();
+    if (warp < h) lists[warp][lane] = warp_merge(lists[warp][lane], lists[warp + h][lane], lane);
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t a) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+
+template <typename T, bool CLUSTER>
+__global__ void __launch_bounds__(kLpThreads) token_logprobs(const LpArgs a) {
+  constexpr int N = Vec<T>::N;
+  __shared__ float s_m[kLpWarps], s_s[kLpWarps], s_t[kLpWarps];
+  __shared__ float s_out[3];
+  __shared__ uint64_t lists[kLpWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int C = CLUSTER ? a.blocks : 1;
+  const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
+  const long long row = blockIdx.x / C;
+  const int stride = C * kLpThreads, me = rank * kLpThreads + static_cast<int>(threadIdx.x);
+  const Row<T> r(static_cast<const T *>(a.x) + row * a.ld, a.V);
+
+  int id = -1;
+  float x_id = 0.f;
+  if (a.ids != nullptr && rank == 0 && threadIdx.x == 0) {
+    id = a.ids[row];
+    if (id >= a.V) {
+      record_status(a.status, AVEY_ERR_DEVICE_BOUNDS);
+      id = -1;
+    }
+    if (id >= 0) x_id = Vec<T>::to_f(r.p[id]);
+  }
+
+  Stat st{kLowest, 0.f, 0.f};
+  float best = -INFINITY;
+  int best_vec = 0;
+  for (int u0 = me; u0 < r.vecs; u0 += kBatch * stride) {
+    uint4 w[kBatch];
+    float v[kBatch][N];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const long long u = u0 + static_cast<long long>(i) * stride;
+      if (u < r.vecs && r.whole(static_cast<int>(u))) w[i] = r.load_whole(static_cast<int>(u));
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const long long u = u0 + static_cast<long long>(i) * stride;
+      if (u < r.vecs && r.whole(static_cast<int>(u))) {
+        Vec<T>::unpack(w[i], v[i]);
+      } else if (u < r.vecs) {
+        r.load_part(static_cast<int>(u), v[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[i][j] = -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      float vm = v[i][0];
+#pragma unroll
+      for (int j = 1; j < N; ++j) vm = fmaxf(vm, v[i][j]);
+      if (vm > best) {
+        best = vm;
+        best_vec = u0 + i * stride;
+      }
+    }
+    if (best > st.m) rebase(st, best);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float d = v[i][j] - st.m, e = fast_exp(d);
+        st.s += e;
+        st.t = fmaf(e, fmaxf(d, kFar), st.t);
+      }
+    }
+  }
+
+  // ---- the row's (m, s, t)
+  const uint64_t my_key = best > -INFINITY ? key_of(best, static_cast<uint32_t>(best_vec)) : 0ull;
+  rebase(st, warp_max(st.m));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
+    st.t += __shfl_xor_sync(0xffffffffu, st.t, off);
+  }
+  if (lane == 0) {
+    s_m[warp] = st.m;
+    s_s[warp] = st.s;
+    s_t[warp] = st.t;
+  }
+  if (a.top > 0) {
+    lists[warp][lane] = warp_sort(my_key, lane);
+    block_merge(lists, warp, lane);
+  } else {
+    __syncthreads();
+  }
+  float M = s_m[0];
+#pragma unroll
+  for (int i = 1; i < kLpWarps; ++i) M = fmaxf(M, s_m[i]);
+  Stat all{M, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kLpWarps; ++i) {
+    Stat o{s_m[i], s_s[i], s_t[i]};
+    rebase(o, M);
+    all.s += o.s;
+    all.t += o.t;
+  }
+  if constexpr (CLUSTER) {
+    if (threadIdx.x == 0) {
+      s_out[0] = all.m;
+      s_out[1] = all.s;
+      s_out[2] = all.t;
+    }
+    __syncwarp();
+    cluster_sync_all();
+    const uint32_t addr = smem_u32(s_out), laddr = smem_u32(&lists[0][lane]);
+    Stat part[8];
+    float CM = kLowest;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      part[c] = Stat{kLowest, 0.f, 0.f};
+      if (c < C) {
+        const uint32_t at = mapa_shared(addr, c);
+        part[c] = Stat{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)};
+      }
+      CM = fmaxf(CM, part[c].m);
+    }
+    all = Stat{CM, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      rebase(part[c], CM);
+      all.s += part[c].s;
+      all.t += part[c].t;
+    }
+    if (a.top > 0) {
+      uint64_t key = 0;
+      if (warp == 0)
+        for (int c = 0; c < C; ++c) key = warp_merge(key, ld_cluster_u64(mapa_shared(laddr, c)), lane);
+      __syncwarp();
+      cluster_sync_all();  // every block has read the lists
+      if (warp == 0) lists[0][lane] = key;
+      __syncthreads();
+    }
+  }
+  const bool empty = all.s == 0.f;
+  // a finite row has 1 <= s <= V; +inf or NaN leave an infinite maximum or a NaN sum
+  const bool bad = !(all.s < INFINITY) || all.m == INFINITY;
+  const float nan = __uint_as_float(0x7fc00000u);
+  const float z = logf(all.s);
+  if (rank == 0 && threadIdx.x == 0) {
+    if (a.logprob)
+      a.logprob[row] = id < 0 ? 0.f : bad ? nan : empty ? -INFINITY : (x_id - all.m) - z;
+    if (a.stats)
+      reinterpret_cast<float2 *>(a.stats)[row] =
+          bad ? make_float2(nan, nan) : empty ? make_float2(-INFINITY, 0.f) : make_float2(all.m, z);
+    if (a.entropy) a.entropy[row] = bad ? nan : empty ? 0.f : z - all.t / all.s;
+  }
+
+  // ---- alternatives
+  if (a.top > 0) {
+    const uint64_t last = lists[0][a.top - 1];
+    const uint32_t bar = last ? static_cast<uint32_t>(last >> 32) : kOrdNegInf + 1u;
+    uint64_t list = 0;  // this warp's best, descending over the lanes
+    int turn = 0;
+    for (int i = 0; i < a.top; ++i) {
+      const uint64_t k = lists[0][i];
+      if (k == 0) break;
+      const int owner = static_cast<int>(~static_cast<uint32_t>(k) % static_cast<uint32_t>(stride));
+      if (owner / kLpThreads != rank || (turn++ & (kLpWarps - 1)) != warp) continue;
+      for (long long u0 = owner; u0 < r.vecs; u0 += 32ll * stride) {
+        const long long u = u0 + static_cast<long long>(lane) * stride;
+        float v[N];
+        if (u < r.vecs) {
+          r.load(static_cast<int>(u), v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[j] = -INFINITY;
+        }
+        const uint64_t full = __shfl_sync(0xffffffffu, list, 31);
+        uint32_t want = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          if (v[j] > -INFINITY && ord_of(v[j]) >= bar &&
+              key_of(v[j], static_cast<uint32_t>(r.first(static_cast<int>(u)) + j)) > full)
+            want |= 1u << j;
+        }
+        uint32_t lanes = __ballot_sync(0xffffffffu, want != 0);
+        while (lanes) {
+          const int src = __ffs(lanes) - 1;
+          uint64_t mine = 0;
+          if (lane == src) {
+            const int j = __ffs(want) - 1;
+            float f = v[0];
+#pragma unroll
+            for (int q = 1; q < N; ++q) f = q == j ? v[q] : f;
+            mine = key_of(f, static_cast<uint32_t>(r.first(static_cast<int>(u)) + j));
+            want &= want - 1;
+          }
+          const uint64_t nk = __shfl_sync(0xffffffffu, mine, src);
+          const int pos = __popc(__ballot_sync(0xffffffffu, list > nk));
+          const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
+          if (lane >= pos) list = lane == pos ? nk : up;
+          lanes = __ballot_sync(0xffffffffu, want != 0);
+        }
+      }
+    }
+    __syncthreads();  // every warp is past lists[0]
+    lists[warp][lane] = list;
+    block_merge(lists, warp, lane);
+    uint64_t key = lists[0][lane];
+    if constexpr (CLUSTER) {
+      __syncwarp();
+      cluster_sync_all();
+      if (rank == 0 && warp == 0) {
+        const uint32_t laddr = smem_u32(&lists[0][lane]);
+        for (int c = 1; c < C; ++c) key = warp_merge(key, ld_cluster_u64(mapa_shared(laddr, c)), lane);
+      }
+    }
+    if (rank == 0 && warp == 0 && lane < a.top) {
+      const bool has = !bad && key != 0;
+      a.top_ids[row * a.top + lane] = has ? static_cast<int32_t>(~static_cast<uint32_t>(key)) : -1;
+      a.top_lp[row * a.top + lane] =
+          bad ? nan : has ? (ord_value(static_cast<uint32_t>(key >> 32)) - all.m) - z : -INFINITY;
+    }
+  }
+  if constexpr (CLUSTER) {
+    __syncwarp();
+    cluster_sync_all();  // no block leaves while its memory is read
+  }
+}
+
+template <typename T>
+avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
+  // few rows: several blocks a row, as long as each thread still has a vector
+  const int sms = sm_count();
+  const long long vecs = (a.V + Vec<T>::N - 1) / Vec<T>::N;
+  int C = 1;
+  while (C < 8 && static_cast<long long>(rows) * C * 2 <= 2ll * sms && vecs >= 2ll * C * kLpThreads) C *= 2;
+  a.blocks = C;
+  if (C == 1) {
+    token_logprobs<T, false><<<rows, kLpThreads, 0, s>>>(a);
+  } else {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows) * C);
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = C;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, token_logprobs<T, true>, static_cast<const LpArgs>(a));
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      set_detail("token_logprobs launch failed: %s", cudaGetErrorString(e));
+      return AVEY_ERR_CUDA;
+    }
+  }
+  AVEY_CHECK_LAUNCH("token_logprobs", s);
+  return AVEY_OK;
+}
+
+// ---- backward ---------------------------------------------------------------
+
+struct LpGradArgs {
+  const void *x;
+  long long ld;
+  int V, parts;  // blocks of a row
+  const int32_t *ids;
+  const float *stats, *entropy, *d_logprob, *d_entropy;
+  void *dx;
+  long long ld_d;
+  int *status;
+};
+
+constexpr int kGradVecs = 8;  // vectors a thread takes at most
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads) token_logprobs_grad(const LpGradArgs a) {
+  constexpr int N = Vec<T>::N;
+  const long long row = blockIdx.x / a.parts;
+  const int part = static_cast<int>(blockIdx.x - row * a.parts);
+  const Row<T> r(static_cast<const T *>(a.x) + row * a.ld, a.V);
+  T *out = static_cast<T *>(a.dx) + row * a.ld_d;
+  // whole vectors of x are whole 16-byte words of the gradient too
+  const bool same = ((reinterpret_cast<uintptr_t>(r.p) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+  int id = a.d_logprob ? a.ids[row] : -1;
+  if (id >= a.V) {
+    if (part == 0 && threadIdx.x == 0) record_status(a.status, AVEY_ERR_DEVICE_BOUNDS);
+    id = -1;
+  }
+  const float g = id >= 0 ? a.d_logprob[row] : 0.f;
+  const float h = a.d_entropy ? a.d_entropy[row] : 0.f;
+  const float2 st = reinterpret_cast<const float2 *>(a.stats)[row];
+  const float H = a.d_entropy ? a.entropy[row] : 0.f;
+  const bool none = (g == 0.f && h == 0.f) || st.x == -INFINITY;
+  const int per = (r.vecs + a.parts - 1) / a.parts;
+  const int end = min(r.vecs, (part + 1) * per);
+  for (int u = part * per + static_cast<int>(threadIdx.x); u < end; u += kLpThreads) {
+    const int e0 = r.first(u);
+    float v[N];
+    if (none) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = 0.f;
+    } else {
+      r.load(u, v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float lp = (v[j] - st.x) - st.y, p = fast_exp(lp);
+        v[j] = -p * fmaf(h, fmaxf(lp, kFar) + H, g);
+        if (e0 + j == id) v[j] += g;
+      }
+    }
+    if (same && r.whole(u)) {
+      *reinterpret_cast<uint4 *>(out + e0) = Vec<T>::pack(v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (e0 + j >= 0 && e0 + j < a.V) out[e0 + j] = Vec<T>::from_f(v[j]);
+    }
+  }
+}
+
+template <typename T>
+avey_status run_logprobs_grad(LpGradArgs a, int rows, cudaStream_t s) {
+  const long long vecs = (static_cast<long long>(a.V) + 2 * Vec<T>::N - 2) / Vec<T>::N;
+  long long parts = (vecs + kGradVecs * kLpThreads - 1) / (kGradVecs * kLpThreads);
+  parts = std::max<long long>(1, std::min<long long>(parts, 0x7fffffffll / rows));
+  a.parts = static_cast<int>(parts);
+  token_logprobs_grad<T><<<static_cast<unsigned>(rows * parts), kLpThreads, 0, s>>>(a);
+  AVEY_CHECK_LAUNCH("token_logprobs_grad", s);
+  return AVEY_OK;
+}
+
+avey_status check_logits(const char *fn, avey_dtype dt, int rows, int V, int64_t ld, const void *x) {
+  AVEY_REQUIRE(dt == AVEY_F32 || dt == AVEY_BF16, AVEY_ERR_UNSUPPORTED,
+               "%s: dtype %d unsupported (F32 or BF16)", fn, int(dt));
+  AVEY_REQUIRE(rows >= 0 && V >= 1, AVEY_ERR_INVALID_ARG, "%s: need rows >= 0 and V >= 1 (rows=%d V=%d)",
+               fn, rows, V);
+  AVEY_REQUIRE(ld >= V, AVEY_ERR_INVALID_ARG, "%s: leading dimension %lld < V=%d", fn,
+               static_cast<long long>(ld), V);
+  AVEY_REQUIRE(rows < (1 << 28) && V <= (1 << 30), AVEY_ERR_UNSUPPORTED,
+               "%s: problem too large (rows=%d V=%d)", fn, rows, V);
+  AVEY_REQUIRE((reinterpret_cast<uintptr_t>(x) & (dt == AVEY_F32 ? 3 : 1)) == 0, AVEY_ERR_INVALID_ARG,
+               "%s: logits are not aligned to their element", fn);
+  return AVEY_OK;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7) == 0; }
+
+}  // namespace
+
+avey_status launch_token_logprobs(const void *logits, avey_dtype dt, int rows, int V, int64_t ld,
+                                  const int32_t *ids, int top, float *logprob, float *stats,
+                                  float *entropy, int32_t *top_ids, float *top_lp, cudaStream_t s) {
+  if (rows == 0) return AVEY_OK;
+  LpArgs a{};
+  a.x = logits;
+  a.ld = ld;
+  a.V = V;
+  a.ids = ids;
+  a.top = top;
+  a.logprob = logprob;
+  a.stats = stats;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_lp = top_lp;
+  a.status = device_status_word();
+  return dt == AVEY_F32 ? run_logprobs<float>(a, rows, s) : run_logprobs<bf16>(a, rows, s);
+}
+
+}  // namespace avey
+
+using namespace avey;
+
+extern "C" avey_status avey_token_logprobs(const void *logits, avey_dtype dt, int rows, int V,
+                                           int64_t ld, const int32_t *ids, int top, float *logprob,
+                                           float *stats, float *entropy, int32_t *top_ids,
+                                           float *top_logprobs, avey_stream_t stream) {
+  const avey_status st = check_logits("avey_token_logprobs", dt, rows, V, ld, logits);
+  if (st != AVEY_OK) return st;
+  AVEY_REQUIRE(top >= 0 && top <= 32, top < 0 ? AVEY_ERR_INVALID_ARG : AVEY_ERR_UNSUPPORTED,
+               "avey_token_logprobs: top=%d outside [0, 32]", top);
+  if (rows == 0) return AVEY_OK;
+  AVEY_REQUIRE(logits, AVEY_ERR_INVALID_ARG, "avey_token_logprobs: null logits");
+  AVEY_REQUIRE((ids != nullptr) == (logprob != nullptr), AVEY_ERR_INVALID_ARG,
+               "avey_token_logprobs: ids and logprob go together");
+  AVEY_REQUIRE((top > 0) == (top_ids != nullptr) && (top > 0) == (top_logprobs != nullptr),
+               AVEY_ERR_INVALID_ARG, "avey_token_logprobs: top=%d and its outputs do not match", top);
+  AVEY_REQUIRE(logprob || stats || entropy || top > 0, AVEY_ERR_INVALID_ARG,
+               "avey_token_logprobs: no output");
+  AVEY_REQUIRE(aligned4(ids) && aligned4(logprob) && aligned8(stats) && aligned4(entropy) &&
+                   aligned4(top_ids) && aligned4(top_logprobs),
+               AVEY_ERR_INVALID_ARG, "avey_token_logprobs: stats 8-byte, other rows 4-byte aligned");
+  return launch_token_logprobs(logits, dt, rows, V, ld, ids, top, logprob, stats, entropy, top_ids,
+                               top_logprobs, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" avey_status avey_token_logprobs_backward(const void *logits, avey_dtype dt, int rows, int V,
+                                                    int64_t ld, const int32_t *ids, const float *stats,
+                                                    const float *entropy, const float *d_logprob,
+                                                    const float *d_entropy, void *dlogits,
+                                                    int64_t ld_d, avey_stream_t stream) {
+  const char *fn = "avey_token_logprobs_backward";
+  const avey_status st = check_logits(fn, dt, rows, V, ld, logits);
+  if (st != AVEY_OK) return st;
+  AVEY_REQUIRE(ld_d >= V, AVEY_ERR_INVALID_ARG, "%s: leading dimension %lld < V=%d", fn,
+               static_cast<long long>(ld_d), V);
+  if (rows == 0) return AVEY_OK;
+  AVEY_REQUIRE(logits && stats && dlogits, AVEY_ERR_INVALID_ARG, "%s: null pointer", fn);
+  AVEY_REQUIRE(!d_logprob || ids, AVEY_ERR_INVALID_ARG, "%s: d_logprob needs ids", fn);
+  AVEY_REQUIRE(!d_entropy || entropy, AVEY_ERR_INVALID_ARG, "%s: d_entropy needs entropy", fn);
+  AVEY_REQUIRE((reinterpret_cast<uintptr_t>(dlogits) & (dt == AVEY_F32 ? 3 : 1)) == 0 && aligned4(ids) &&
+                   aligned8(stats) && aligned4(entropy) && aligned4(d_logprob) && aligned4(d_entropy),
+               AVEY_ERR_INVALID_ARG, "%s: dlogits aligned to its element, stats 8-byte, rows 4-byte", fn);
+  {
+    const uintptr_t es = dt == AVEY_F32 ? 4 : 2;
+    const uintptr_t x0 = reinterpret_cast<uintptr_t>(logits), d0 = reinterpret_cast<uintptr_t>(dlogits);
+    const uintptr_t xn = x0 + (static_cast<uintptr_t>(rows - 1) * ld + V) * es;
+    const uintptr_t dn = d0 + (static_cast<uintptr_t>(rows - 1) * ld_d + V) * es;
+    AVEY_REQUIRE((x0 == d0 && ld == ld_d) || dn <= x0 || xn <= d0, AVEY_ERR_INVALID_ARG,
+                 "%s: dlogits overlaps the logits without being them", fn);
+  }
+  LpGradArgs a{};
+  a.x = logits;
+  a.ld = ld;
+  a.V = V;
+  a.ids = ids;
+  a.stats = stats;
+  a.entropy = entropy;
+  a.d_logprob = d_logprob;
+  a.d_entropy = d_entropy;
+  a.dx = dlogits;
+  a.ld_d = ld_d;
+  a.status = device_status_word();
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return dt == AVEY_F32 ? run_logprobs_grad<float>(a, rows, s) : run_logprobs_grad<bf16>(a, rows, s);
+}

@@ -46,6 +46,8 @@
  *               after the hi plane (plane stride = rows * ld elements).  Layer
  *               activations use it so that products against bf16 weights
  *               keep about 16 significant bits.
+ *   AVEY_I8     8-bit integers with an fp32 scale per row (avey_quantize_rows);
+ *               taken by the 8-bit products only.
  */
 #ifndef AVEY_H_
 #define AVEY_H_
@@ -74,7 +76,7 @@ typedef enum {
   AVEY_ERR_DEVICE_BOUNDS = 5   /* a kernel's bounds check failed (reported by avey_device_status) */
 } avey_status;
 
-typedef enum { AVEY_F32 = 0, AVEY_BF16 = 1, AVEY_BF16X2 = 2 } avey_dtype;
+typedef enum { AVEY_F32 = 0, AVEY_BF16 = 1, AVEY_BF16X2 = 2, AVEY_I8 = 3 } avey_dtype;
 
 /* Contextualizer kinds: the two Avey-B layers, plus the coupled causal layer
  * of the original (autoregressive) Avey for comparison. */
@@ -346,6 +348,134 @@ AVEY_API size_t avey_layer_workspace_bytes(avey_dtype dt, int T, int d, int m, i
  * bf16 split pair, 4 S^2 bytes per block) and two fp32 scales per token. */
 AVEY_API size_t avey_layer_workspace_bytes_ex(avey_dtype dt, int T, int d, int m, int prenorm, int S,
                                               avey_ctx_kind kind);
+
+/* ------------------------------------------------------- 8-bit products --
+ * Products in 8-bit integers with a scale for each token and each output
+ * channel, for serving the layers and a vocabulary head at half the bytes and
+ * twice the tensor rate of bf16.  The pages have no counterpart.
+ *
+ * avey_quantize_rows: rows of x as 8-bit integers and one fp32 scale per row:
+ *   s = fl32(max_j |x_j| * fl32(1 / 127)),  q_j = x_j / s rounded to the nearest integer
+ *   (ties to even; the exact quotient decides), clamped to [-127, 127]
+ *   scale = s, or with prenorm s / sqrt(mean(x^2) + 1e-6): the row stands for
+ *   scale * q, the (RMS-normalised) row to within s / 2 a value.
+ * A row of zeros gets s = 0 and q = 0.  A row holding a NaN or an infinity
+ * gets the scale NaN and q = 0, so that all its products are NaN.
+ *
+ * x      [rows, cols], leading dimension ld_x; AVEY_F32, AVEY_BF16 or
+ *        AVEY_BF16X2 (lo plane rows * ld_x elements after hi).  Aligned to its
+ *        element; 16-byte aligned rows are read in 16-byte words.
+ * q      [rows, ld_q] out; columns cols .. roundup16(cols)-1 are set to 0, those
+ *        behind are left as they were.  16-byte aligned, ld_q % 16 == 0.
+ * scale  [rows] fp32 out.
+ * Constraints: rows >= 0 (0: nothing is done), cols >= 1, ld_x >= cols,
+ * ld_q >= cols.
+ */
+AVEY_API avey_status avey_quantize_rows(const void *x, avey_dtype dt, int rows, int cols,
+                                        int64_t ld_x, int prenorm, int8_t *q, int64_t ld_q,
+                                        float *scale, avey_stream_t stream);
+
+/* avey_linear_i8:
+ *   y_tn = act(s_t w_n sum_k q_tk Wq_nk + b_n) + r_tn
+ * with an exact int32 sum, everything after it in fp32 and one rounding to the
+ * output type.
+ *
+ * p       Wq [N, ld_w] int8 (row n: output channel n; columns >= K are not
+ *         used), w_scale [N] and bias [N] (NULL: 0) fp32.  act AVEY_ACT_NONE or
+ *         AVEY_ACT_RELU2 (max(y, 0)^2, the enricher's).
+ * x       [rows, K], leading dimension ld_x.  AVEY_I8: already quantised, with
+ *         x_scale [rows].  AVEY_F32, AVEY_BF16, AVEY_BF16X2: quantised as
+ *         avey_quantize_rows does (prenorm included) within the call; x_scale
+ *         must be NULL.
+ * residual [rows, N] fp32 with leading dimension ld_out, or NULL.  Needs an
+ *         AVEY_F32 output, which may be the residual itself.
+ * out     [rows, N], leading dimension ld_out; AVEY_F32, AVEY_BF16 or
+ *         AVEY_BF16X2 (lo plane rows * ld_out elements after hi).  Columns >= N
+ *         are left as they were.
+ * ws      at least avey_linear_i8_workspace_bytes(...) bytes, 256-byte aligned
+ *         (may be NULL when that is 0).
+ * Constraints: rows >= 0 (0: nothing is done), K, N >= 1, K <= 131071 (the
+ * int32 sum); ld_w % 16 == 0, ld_x % 16 == 0 for AVEY_I8, ld_out % 8 == 0;
+ * Wq, w_scale, bias, out, residual and AVEY_I8 x 16-byte aligned.  out must not
+ * overlap any other buffer of the call.
+ */
+enum { AVEY_ACT_NONE = 0, AVEY_ACT_RELU2 = 1 };
+
+typedef struct {
+  int K, N;
+  const int8_t *Wq;
+  int64_t ld_w;
+  const float *w_scale;
+  const float *bias;
+  int act;
+} avey_linear_i8_params;
+
+AVEY_API avey_status avey_linear_i8(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt,
+                                    int64_t ld_x, const float *x_scale, int prenorm, int rows,
+                                    const float *residual, void *out, avey_dtype out_dt,
+                                    int64_t ld_out, void *ws, size_t ws_bytes, avey_stream_t stream);
+
+AVEY_API size_t avey_linear_i8_workspace_bytes(avey_dtype x_dt, int rows, int K);
+
+/* -------------------------------------------------------- token scoring --
+ * avey_token_logprobs: per row of logits over a vocabulary of V words
+ *   m = max_j x_j,  z = log sum_j exp(x_j - m)        stats = (m, z)
+ *   logprob  = x_id - m - z                           of the given token
+ *   entropy  = -sum_j p_j log p_j,  p_j = exp(x_j - m - z)
+ *   the `top` words of highest logit, by (logit desc, index asc), and their
+ *   log probabilities
+ * from one pass over the logits.  Sums are fp32.
+ *   - An entry of -inf has probability 0 and is never an alternative.  Fewer
+ *     than `top` others: the rest are -1 and -inf.
+ *   - ids < 0: no given token, logprob 0.  ids >= V are rejected on the device
+ *     (AVEY_ERR_DEVICE_BOUNDS) and treated as none.
+ *   - A row of -inf alone: stats (-inf, 0), entropy 0, logprob -inf.
+ *   - A row holding NaN or +inf: NaN everywhere, alternatives -1.
+ * logits  [rows, V], leading dimension ld, AVEY_F32 or AVEY_BF16, aligned to
+ *         its element (rows on 16-byte boundaries are read fastest).
+ * ids     [rows] int32, with logprob [rows] fp32 out; both NULL for neither.
+ * stats   [rows, 2] fp32 out or NULL;  entropy [rows] fp32 out or NULL.
+ * top_ids [rows, top] int32, top_logprobs [rows, top] fp32 out (top > 0).
+ * Constraints: rows >= 0 (0: nothing is done), V >= 1, ld >= V, 0 <= top <= 32,
+ * rows * 8 < 2^31.
+ */
+AVEY_API avey_status avey_token_logprobs(const void *logits, avey_dtype dt, int rows, int V,
+                                         int64_t ld, const int32_t *ids, int top, float *logprob,
+                                         float *stats, float *entropy, int32_t *top_ids,
+                                         float *top_logprobs, avey_stream_t stream);
+
+/* avey_token_logprobs_backward: the gradient of sum_t (d_logprob_t logprob_t +
+ * d_entropy_t entropy_t) with respect to the logits,
+ *   dx_j = g (1[j = id] - p_j) - h p_j (log p_j + entropy),
+ * g = d_logprob (0 where there is no given token), h = d_entropy.
+ * logits, ids, stats and entropy as given to and written by
+ * avey_token_logprobs.  d_logprob (with ids) or d_entropy (with entropy) may be
+ * NULL for 0.  A row with g = h = 0 gets zeros whatever its logits hold, a row
+ * of -inf alone too; -inf entries get 0.
+ * dlogits [rows, V], type of the logits, leading dimension ld_d; may be the
+ *         logits themselves (same ld), no partial overlap.
+ * Constraints as avey_token_logprobs.
+ */
+AVEY_API avey_status avey_token_logprobs_backward(const void *logits, avey_dtype dt, int rows, int V,
+                                                  int64_t ld, const int32_t *ids, const float *stats,
+                                                  const float *entropy, const float *d_logprob,
+                                                  const float *d_entropy, void *dlogits, int64_t ld_d,
+                                                  avey_stream_t stream);
+
+/* avey_score_tokens_i8: avey_linear_i8 against a vocabulary matrix (p->N words,
+ * act AVEY_ACT_NONE), then logprob, stats and entropy of its rows as
+ * avey_token_logprobs defines them, on logits that are not rounded below fp32
+ * and not an output.  x, x_dt, ld_x, x_scale, prenorm as avey_linear_i8;
+ * outputs as avey_token_logprobs (any may be NULL, not all).
+ * ws: at least avey_score_tokens_i8_workspace_bytes(...) bytes, 256-byte
+ * aligned. */
+AVEY_API avey_status avey_score_tokens_i8(const avey_linear_i8_params *p, const void *x,
+                                          avey_dtype x_dt, int64_t ld_x, const float *x_scale,
+                                          int prenorm, int rows, const int32_t *ids, float *logprob,
+                                          float *stats, float *entropy, void *ws, size_t ws_bytes,
+                                          avey_stream_t stream);
+
+AVEY_API size_t avey_score_tokens_i8_workspace_bytes(int rows, int K, int N);
 
 /* ------------------------------------------------------------- utilities --
  * avey_device_status: synchronises `stream`, returns the first kernel-side
