@@ -15,19 +15,28 @@ namespace avey {
 namespace {
 
 constexpr int kBK = 128;
-constexpr int kLinEpi = 4, kLinThreads = 64 + 32 * kLinEpi;
+constexpr int kLinEpi = 8, kLinThreads = 64 + 32 * kLinEpi;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kFar2 = -200.0f;  // ex2 is 0 in fp32 from here down
 
-template <int BN>
+// What the epilogue does with the products besides AVEY_F32, AVEY_BF16 and
+// AVEY_BF16X2 (stores): running softmax statistics of each row.
+constexpr int kScore = -1;
+
+template <int BN, int OUT>
 struct LinLayout {
   static constexpr int PM = 256;
   static constexpr uint32_t A_BYTES = 128 * kBK;        // this CTA's rows
   static constexpr uint32_t B_BYTES = (BN / 2) * kBK;   // this CTA's half of the channels
   static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr uint32_t BUF = OUT == kScore ? 0 : OUT == AVEY_BF16 ? 2048 : 4096;
+  static constexpr int STAGES = BN < 256 ? 6 : OUT == kScore ? 6 : OUT == AVEY_BF16 ? 5 : 4;
   static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES;
   static constexpr uint32_t CTRL_BYTES = 1024;
-  static constexpr uint32_t STAGING_BYTES = kLinEpi * 8192;
-  static constexpr uint32_t SMEM_BYTES = TILES_BYTES + CTRL_BYTES + STAGING_BYTES + 1024;
+  static constexpr uint32_t COLS_BYTES = 2 * 2 * BN * 4;  // scale and bias, two tiles
+  static constexpr uint32_t STAGING_BYTES = kLinEpi * 2 * BUF;
+  static constexpr uint32_t SMEM_BYTES = TILES_BYTES + STAGING_BYTES + CTRL_BYTES + COLS_BYTES + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(STAGES <= 8, "the control block holds at most 8 stages");
@@ -45,6 +54,7 @@ struct LinArgs {
   int N_tma;
   void *out;
   long long ld_out;
+  float4 *partial;  // kScore: (max, sum, weighted sum) of a row's share of the words
   int *status;
 };
 
@@ -62,15 +72,54 @@ __device__ __forceinline__ void lin_st4(uint32_t addr, uint32_t a, uint32_t b, u
                : "memory");
 }
 
-// Four consecutive fp32 of a row of n, zeros past its end; p + i 16-byte aligned.
-__device__ __forceinline__ float4 load4(const float *p, int i, int n) {
-  if (i + 4 <= n) return __ldg(reinterpret_cast<const float4 *>(p + i));
-  return make_float4(i < n ? p[i] : 0.f, i + 1 < n ? p[i + 1] : 0.f, i + 2 < n ? p[i + 2] : 0.f, 0.f);
-}
-// The same without the read-only path, for a residual that the call overwrites.
+// Four consecutive fp32 of a residual row of n, zeros past its end (plain
+// loads: the call may overwrite it).
 __device__ __forceinline__ float4 load4_rw(const float *p, int i, int n) {
   if (i + 4 <= n) return *reinterpret_cast<const float4 *>(p + i);
   return make_float4(i < n ? p[i] : 0.f, i + 1 < n ? p[i + 1] : 0.f, i + 2 < n ? p[i + 2] : 0.f, 0.f);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
+  return *reinterpret_cast<const float2 *>(&r);
+}
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)),
+        "l"(*reinterpret_cast<const uint64_t *>(&c)));
+  return *reinterpret_cast<const float2 *>(&r);
+}
+
+// (max, sum 2^(y - max), sum 2^(y - max) (y - max)) of values y in units of log 2
+struct Stat2 {
+  float m, s, t;
+};
+__device__ __forceinline__ void rebase2(Stat2 &a, float M) {
+  const float d = a.m - M, f = ex2(d);
+  a.t = f * fmaf(a.s, fmaxf(d, kFar2), a.t);
+  a.s *= f;
+  a.m = M;
+}
+
+// First tile of pair p's share of the scoring: shares are contiguous in the
+// order (row block, word block).
+__host__ __device__ __forceinline__ long long score_start(long long p, long long tiles, int npairs) {
+  return p * tiles / npairs;
 }
 
 // The columns from N_tma of a row's 32-column chunk.
@@ -95,18 +144,75 @@ __device__ __forceinline__ void store_rest(const LinArgs &a, int row, int col0, 
   }
 }
 
+// Scale, bias and activation of a 32-column chunk of int32 sums; w and b are
+// the chunk's columns in shared memory.
+__device__ __forceinline__ void lin_values(float (&v)[32], float xs, const float *w, const float *b,
+                                           int relu2) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float4 w4 = *reinterpret_cast<const float4 *>(w + 4 * q);
+    const float4 b4 = *reinterpret_cast<const float4 *>(b + 4 * q);
+    const float ww[4] = {w4.x, w4.y, w4.z, w4.w}, bb[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[4 * q + j] = fmaf(static_cast<float>(__float_as_int(v[4 * q + j])) * xs, ww[j], bb[j]);
+  }
+  if (relu2) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float y = max_nan(v[j], 0.f);  // NaN stays NaN
+      v[j] = y * y;
+    }
+  }
+}
+
+// A 32-column chunk into a row's running statistics.
+__device__ __forceinline__ void score_values(float (&v)[32], float xs, const float *w, const float *b,
+                                             Stat2 &st) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float4 w4 = *reinterpret_cast<const float4 *>(w + 4 * q);
+    const float4 b4 = *reinterpret_cast<const float4 *>(b + 4 * q);
+    const float2 x2 = make_float2(xs, xs);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 f = make_float2(static_cast<float>(__float_as_int(v[4 * q + 2 * h])),
+                                   static_cast<float>(__float_as_int(v[4 * q + 2 * h + 1])));
+      const float2 y = ffma2(fmul2(f, x2), h ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y),
+                             h ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y));
+      v[4 * q + 2 * h] = y.x;
+      v[4 * q + 2 * h + 1] = y.y;
+    }
+  }
+  rebase2(st, fmaxf(st.m, max32(v)));
+  const float2 minus = make_float2(-st.m, -st.m);
+  float2 s = make_float2(0.f, 0.f), t = s;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float2 d = fadd2(make_float2(v[2 * j], v[2 * j + 1]), minus);
+    d.x = max_nan(d.x, kFar2);
+    d.y = max_nan(d.y, kFar2);
+    const float2 e = make_float2(ex2(d.x), ex2(d.y));
+    s = fadd2(s, e);
+    t = ffma2(e, d, t);
+  }
+  st.s += s.x + s.y;
+  st.t += t.x + t.y;
+}
+
 template <int BN, int OUT, bool RES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     linear_i8_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
                    const LinArgs a) {
-  using P = LinLayout<BN>;
+  using P = LinLayout<BN, OUT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
-  uint8_t *ctrl = smem_raw + pad + P::TILES_BYTES;
+  uint8_t *ctrl = smem_raw + pad + P::TILES_BYTES + P::STAGING_BYTES;
   const uint32_t sbase = raw_s + pad;
-  const uint32_t cbase = sbase + P::TILES_BYTES;
+  const uint32_t cbase = sbase + P::TILES_BYTES + P::STAGING_BYTES;
+  float *cols = reinterpret_cast<float *>(ctrl + P::CTRL_BYTES);  // [2 tiles][scale, bias][BN]
   // control block: full[8] @0, empty[8] @64, tfull[2] @128, tempty[2] @144,
   // drain @160, tmem base @168, abort flag @172
   auto full_bar = [&](int s) { return cbase + 8u * s; };
@@ -120,6 +226,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  // Tiles of this pair: dealt round robin, or for the scores a contiguous
+  // share, so that a row's statistics stay in one thread's registers.
+  const long long t_first = OUT == kScore ? score_start(pair, a.num_tiles, npairs) : pair;
+  const long long t_end = OUT == kScore ? score_start(pair + 1, a.num_tiles, npairs) : a.num_tiles;
+  const long long t_step = OUT == kScore ? 1 : npairs;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < P::STAGES; ++s) {
@@ -137,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
-    prefetch_tmap(&tmO0);
+    if (OUT != kScore) prefetch_tmap(&tmO0);
     if (OUT == AVEY_BF16X2) prefetch_tmap(&tmO1);
   }
   cluster_sync_all();
@@ -158,7 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       uint32_t phase = 0;
       long long issued = 0;
       bool ok = true;
-      for (long long tile = pair; ok && tile < a.num_tiles; tile += npairs) {
+      for (long long tile = t_first; ok && tile < t_end; tile += t_step) {
         const int mt = static_cast<int>(tile / a.tiles_n), nt = static_cast<int>(tile % a.tiles_n);
         const int arow = mt * P::PM + static_cast<int>(rank) * 128;
         const int brow = nt * BN + static_cast<int>(rank) * (BN / 2);
@@ -198,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (long long tile = pair; ok && tile < a.num_tiles; tile += npairs) {
+      for (long long tile = t_first; ok && tile < t_end; tile += t_step) {
         if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag)) {
           ok = false;
           break;
@@ -236,107 +347,138 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
   } else {
     // ------------------------------------------------------------- epilogue
-    const int quarter = warp & 3;  // TMEM lanes 32*quarter .. +31
-    const uint32_t stg = cbase + P::CTRL_BYTES + static_cast<uint32_t>(warp - 2) * 8192u;
+    // Eight warps: a quarter of the CTA's rows (TMEM lanes 32*quarter .. +31)
+    // and every other 32-column chunk each.
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int et = static_cast<int>(threadIdx.x) - 64;  // 0 .. 255
+    const uint32_t stg = sbase + P::TILES_BYTES + static_cast<uint32_t>(warp - 2) * 2u * P::BUF;
     const uint32_t tempty_r0 = mapa_shared(tempty_bar(0), 0), tempty_r1 = mapa_shared(tempty_bar(1), 0);
+    // scale and bias of this thread's column of a tile; the scores work in
+    // units of log 2, and words past the last have the value -inf
+    auto column = [&](long long tile, float &w, float &b) {
+      if (tile >= t_end || et >= BN) return;
+      const int c = static_cast<int>(tile % a.tiles_n) * BN + et;
+      const bool in = c < a.N;
+      w = in ? __ldg(a.w_scale + c) : 0.f;
+      b = in && a.bias ? __ldg(a.bias + c) : 0.f;
+      if constexpr (OUT == kScore) b = in ? b * kLog2e : -INFINITY;
+    };
     int acc = 0, it = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (long long tile = pair; tile < a.num_tiles; tile += npairs) {
+    float cw = 0.f, cb = 0.f;
+    column(t_first, cw, cb);
+    Stat2 st{kLowest, 0.f, 0.f};
+    for (long long tile = t_first; tile < t_end; tile += t_step) {
       const int mt = static_cast<int>(tile / a.tiles_n), nt = static_cast<int>(tile % a.tiles_n);
       const int row0 = mt * P::PM + static_cast<int>(rank) * 128 + quarter * 32;
       const int row = row0 + lane;
       const bool valid = row < a.rows;
-      const float xs = valid ? a.x_scale[row] : 0.f;
-      if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) {
-        ok = false;
-        break;
+      float xs = valid ? __ldg(a.x_scale + row) : 0.f;
+      if constexpr (OUT == kScore) xs *= kLog2e;
+      // Columns of tile i go to buffer i & 1.  A warp here has passed the barrier
+      // of tile i - 1, so every warp is done with tile i - 2, the buffer's last.
+      float *w_s = cols + acc * 2 * BN, *b_s = w_s + BN;
+      if (et < BN) {
+        w_s[et] = cw;
+        b_s[et] = cb;
       }
+      column(tile + t_step, cw, cb);
+      named_bar_sync(1, 32 * kLinEpi);
+      // A warp that gave up still meets the others at the barrier of each tile.
+      if (ok && !mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) {
+        ok = false;
+        *abort_flag = 1;
+      }
+      if (!ok) continue;
       tc_fence_after();
       const uint32_t taddr =
           tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-      for (int ch = 0; ch < BN / 32; ++ch) {
+      for (int ch = half; ch < BN / 32; ch += 2) {
         const int col0 = nt * BN + ch * 32;
         if (col0 >= a.N || row0 >= a.rows) break;  // warp-uniform
-        float v[32];
-        tmem_ld32(taddr + ch * 32, v);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int c = col0 + 4 * q;
-          const float4 w = load4(a.w_scale, c, a.N);
-          const float4 b = a.bias ? load4(a.bias, c, a.N) : make_float4(0.f, 0.f, 0.f, 0.f);
-          const float ww[4] = {w.x, w.y, w.z, w.w}, bb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float y = fmaf(static_cast<float>(__float_as_int(v[4 * q + j])) * xs, ww[j], bb[j]);
-            if (a.relu2) {
-              // written so that NaN stays NaN
-              y = y < 0.f ? 0.f : y;
-              y *= y;
-            }
-            v[4 * q + j] = y;
-          }
-        }
+        float4 res[RES ? 8 : 1];
         if constexpr (RES) {
           const float *rr = a.residual + static_cast<long long>(row) * a.ld_out;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 x = valid ? load4_rw(rr, col0 + 4 * q, a.N) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[4 * q] += x.x;
-            v[4 * q + 1] += x.y;
-            v[4 * q + 2] += x.z;
-            v[4 * q + 3] += x.w;
-          }
+          for (int q = 0; q < 8; ++q)
+            res[q] = valid ? load4_rw(rr, col0 + 4 * q, a.N) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (col0 + 32 > a.N_tma && valid) store_rest<OUT>(a, row, col0, v);
-        if (col0 >= a.N_tma) continue;  // warp-uniform
-        const uint32_t buf = stg + (it & 1) * 4096;
-        if (it >= 2) {  // the store issued from this buffer two chunks ago must have read it
-          if (lane == 0) bulk_wait_read<1>();
-          __syncwarp();
-        }
-        if constexpr (OUT == AVEY_F32) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            lin_st4(buf + lin_sw128(lane, c), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                    __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
-        } else if constexpr (OUT == AVEY_BF16) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            lin_st4(buf + lin_sw64(lane, c), pack_bf16(v[8 * c], v[8 * c + 1]),
-                    pack_bf16(v[8 * c + 2], v[8 * c + 3]), pack_bf16(v[8 * c + 4], v[8 * c + 5]),
-                    pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+        float v[32];
+        tmem_ld32(taddr + ch * 32, v);
+        if constexpr (OUT == kScore) {
+          score_values(v, xs, w_s + ch * 32, b_s + ch * 32, st);
         } else {
-          uint32_t hi[16], lo[16];
+          lin_values(v, xs, w_s + ch * 32, b_s + ch * 32, a.relu2);
+          if constexpr (RES) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) split_pack(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            lin_st4(buf + lin_sw64(lane, c), hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-            lin_st4(buf + 2048 + lin_sw64(lane, c), lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+            for (int q = 0; q < 8; ++q) {
+              v[4 * q] += res[q].x;
+              v[4 * q + 1] += res[q].y;
+              v[4 * q + 2] += res[q].z;
+              v[4 * q + 3] += res[q].w;
+            }
           }
+          if (col0 + 32 > a.N_tma && valid) store_rest<OUT>(a, row, col0, v);
+          if (col0 >= a.N_tma) continue;  // warp-uniform
+          const uint32_t buf = stg + (it & 1) * P::BUF;
+          if (it >= 2) {  // the store issued from this buffer two chunks ago must have read it
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+          }
+          if constexpr (OUT == AVEY_F32) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              lin_st4(buf + lin_sw128(lane, c), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                      __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+          } else if constexpr (OUT == AVEY_BF16) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              lin_st4(buf + lin_sw64(lane, c), pack_bf16(v[8 * c], v[8 * c + 1]),
+                      pack_bf16(v[8 * c + 2], v[8 * c + 3]), pack_bf16(v[8 * c + 4], v[8 * c + 5]),
+                      pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+          } else {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) split_pack(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              lin_st4(buf + lin_sw64(lane, c), hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+              lin_st4(buf + 2048 + lin_sw64(lane, c), lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tmO0, buf, col0, row0, 0);
+            if constexpr (OUT == AVEY_BF16X2) tma_store_3d(&tmO1, buf + 2048, col0, row0, 0);
+            bulk_commit();
+          }
+          ++it;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&tmO0, buf, col0, row0, 0);
-          if constexpr (OUT == AVEY_BF16X2) tma_store_3d(&tmO1, buf + 2048, col0, row0, 0);
-          bulk_commit();
-        }
-        ++it;
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc ? tempty_r1 : tempty_r0);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
+      if constexpr (OUT == kScore) {
+        // the row block or the share ends here: pair p meets row block mt in
+        // slot p + mt alone, since both only grow along the tiles
+        if (nt == a.tiles_n - 1 || tile + 1 == t_end) {
+          const long long slot = static_cast<long long>(pair) + mt;
+          a.partial[slot * 512 + half * 256 + static_cast<int>(rank) * 128 + quarter * 32 + lane] =
+              make_float4(st.m, st.s, st.t, 0.f);
+          st = Stat2{kLowest, 0.f, 0.f};
+        }
+      }
     }
     if (!ok) {
       *abort_flag = 1;
       record_status(a.status, AVEY_ERR_DEVICE_TIMEOUT);
     }
-    if (lane == 0) bulk_wait_all();  // outputs written
+    if (OUT != kScore && lane == 0) bulk_wait_all();  // outputs written
   }
 
   tc_fence_before();
@@ -353,8 +495,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 
 template <int BN, int OUT, bool RES>
 avey_status run_linear_pair(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &o0,
-                            const CUtensorMap &o1, const LinArgs &a, cudaStream_t st) {
-  using P = LinLayout<BN>;
+                            const CUtensorMap &o1, const LinArgs &a, int pairs, cudaStream_t st) {
+  using P = LinLayout<BN, OUT>;
   auto kern = linear_i8_pair<BN, OUT, RES>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(P::SMEM_BYTES));
@@ -363,11 +505,13 @@ avey_status run_linear_pair(const CUtensorMap &ma, const CUtensorMap &mb, const 
     set_detail("linear_i8: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     return AVEY_ERR_CUDA;
   }
-  const int cap = std::max(1, sm_count() / 2);
-  const int pairs = static_cast<int>(std::min<long long>(a.num_tiles, cap));
   kern<<<2 * pairs, kLinThreads, P::SMEM_BYTES, st>>>(ma, mb, o0, o1, a);
-  AVEY_CHECK_LAUNCH("linear_i8", st);
+  AVEY_CHECK_LAUNCH(OUT == kScore ? "score_i8" : "linear_i8", st);
   return AVEY_OK;
+}
+
+inline int pairs_for(long long tiles) {
+  return static_cast<int>(std::min<long long>(tiles, std::max(1, sm_count() / 2)));
 }
 
 template <int BN>
@@ -391,10 +535,11 @@ avey_status run_linear_bn(const avey_linear_i8_params *p, const int8_t *xq, int6
       !encode_map(&o1, false, static_cast<bf16 *>(out) + static_cast<long long>(a.rows) * a.ld_out, inner,
                   a.rows, 1, rs, rs * a.rows, 32, 32, 64))
     return AVEY_ERR_CUDA;
-  if (out_dt == AVEY_BF16) return run_linear_pair<BN, AVEY_BF16, false>(ma, mb, o0, o1, a, s);
-  if (out_dt == AVEY_BF16X2) return run_linear_pair<BN, AVEY_BF16X2, false>(ma, mb, o0, o1, a, s);
-  if (a.residual) return run_linear_pair<BN, AVEY_F32, true>(ma, mb, o0, o1, a, s);
-  return run_linear_pair<BN, AVEY_F32, false>(ma, mb, o0, o1, a, s);
+  const int pairs = pairs_for(a.num_tiles);
+  if (out_dt == AVEY_BF16) return run_linear_pair<BN, AVEY_BF16, false>(ma, mb, o0, o1, a, pairs, s);
+  if (out_dt == AVEY_BF16X2) return run_linear_pair<BN, AVEY_BF16X2, false>(ma, mb, o0, o1, a, pairs, s);
+  if (a.residual) return run_linear_pair<BN, AVEY_F32, true>(ma, mb, o0, o1, a, pairs, s);
+  return run_linear_pair<BN, AVEY_F32, false>(ma, mb, o0, o1, a, pairs, s);
 }
 
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
@@ -505,17 +650,120 @@ extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void
 
 // ------------------------------------------------------------- scoring ------
 
-// Logits of the simple form live in the workspace, in chunks of rows.
-static inline int64_t score_ld(int N) { return (static_cast<int64_t>(N) + 7) / 8 * 8; }
-static inline int score_chunk(int rows, int N) {
-  const int64_t fit = (256ll << 20) / (score_ld(N) * 4);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, std::max<int64_t>(256, fit / 256 * 256))));
+namespace avey {
+namespace {
+
+// One warp per row: joins the row's partial statistics, and computes the given
+// token's logit again from its K bytes of either operand.
+__global__ void __launch_bounds__(256)
+    score_join(const LinArgs a, int npairs, const int8_t *__restrict__ xq, long long ld_xq,
+               const int8_t *__restrict__ Wq, long long ld_w, const int32_t *__restrict__ ids,
+               float *__restrict__ logprob, float *__restrict__ stats, float *__restrict__ entropy) {
+  const int row = blockIdx.x * 8 + static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= a.rows) return;
+  const int mt = row / 256;
+  const long long first = static_cast<long long>(mt) * a.tiles_n, last = first + a.tiles_n - 1;
+  // the pairs whose shares hold tiles first .. last
+  long long p0 = first * npairs / a.num_tiles, p1 = last * npairs / a.num_tiles;
+  while (score_start(p0 + 1, a.num_tiles, npairs) <= first) ++p0;
+  while (score_start(p0, a.num_tiles, npairs) > first) --p0;
+  while (score_start(p1 + 1, a.num_tiles, npairs) <= last) ++p1;
+  while (score_start(p1, a.num_tiles, npairs) > last) --p1;
+  Stat2 st{kLowest, 0.f, 0.f};
+  const int parts = 2 * static_cast<int>(p1 - p0 + 1);
+  for (int i = lane; i < parts; i += 32) {
+    const float4 v = a.partial[(p0 + (i >> 1) + mt) * 512 + (i & 1) * 256 + (row & 255)];
+    Stat2 o{v.x, v.y, v.z};
+    const float M = fmaxf(st.m, o.m);
+    rebase2(st, M);
+    rebase2(o, M);
+    st.s += o.s;
+    st.t += o.t;
+  }
+  rebase2(st, warp_max(st.m));
+  int id = ids ? ids[row] : -1;
+  if (id >= a.N) {
+    if (lane == 0) record_status(a.status, AVEY_ERR_DEVICE_BOUNDS);
+    id = -1;
+  }
+  int acc = 0;
+  if (id >= 0) {
+    const int8_t *x = xq + row * ld_xq, *w = Wq + id * ld_w;
+    const int whole = a.K / 4;
+    for (int i = lane; i < whole; i += 32)
+      acc = __dp4a(reinterpret_cast<const int *>(x)[i], reinterpret_cast<const int *>(w)[i], acc);
+    const int k = whole * 4 + lane;
+    if (k < a.K) acc += static_cast<int>(x[k]) * static_cast<int>(w[k]);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
+    st.t += __shfl_xor_sync(0xffffffffu, st.t, off);
+    acc += __shfl_xor_sync(0xffffffffu, acc, off);
+  }
+  if (lane != 0) return;
+  const bool empty = st.s == 0.f;
+  const bool bad = !(st.s < INFINITY) || st.m == INFINITY;
+  const float nan = __uint_as_float(0x7fc00000u);
+  const float z = logf(st.s);
+  if (logprob) {
+    float lp = 0.f;
+    if (id >= 0) {
+      const float y = fmaf(static_cast<float>(acc) * (a.x_scale[row] * kLog2e), a.w_scale[id],
+                           a.bias ? a.bias[id] * kLog2e : 0.f);
+      lp = bad ? nan : empty ? -INFINITY : fmaf(y - st.m, kLn2, -z);
+    }
+    logprob[row] = lp;
+  }
+  if (stats)
+    reinterpret_cast<float2 *>(stats)[row] =
+        bad ? make_float2(nan, nan) : empty ? make_float2(-INFINITY, 0.f) : make_float2(st.m * kLn2, z);
+  if (entropy) entropy[row] = bad ? nan : empty ? 0.f : fmaf(-kLn2, st.t / st.s, z);
 }
+
+// Up to this many rows the logits go through the workspace, row by row.
+constexpr int kFewRows = 32;
+
+inline int64_t score_ld(int N) { return (static_cast<int64_t>(N) + 7) / 8 * 8; }
+inline size_t score_partial_bytes(int rows) {
+  const size_t slots = static_cast<size_t>((rows + 255) / 256) + std::max(1, sm_count() / 2);
+  return slots * 512 * sizeof(float4);
+}
+
+avey_status launch_score_i8(const avey_linear_i8_params *p, const int8_t *xq, int64_t ld_xq,
+                            const float *x_scale, int rows, const int32_t *ids, float *logprob,
+                            float *stats, float *entropy, float4 *partial, cudaStream_t s) {
+  LinArgs a{};
+  a.rows = rows;
+  a.N = p->N;
+  a.K = p->K;
+  a.x_scale = x_scale;
+  a.w_scale = p->w_scale;
+  a.bias = p->bias;
+  a.partial = partial;
+  a.status = device_status_word();
+  a.tiles_m = (rows + 255) / 256;
+  a.tiles_n = (p->N + 255) / 256;
+  a.num_tiles = static_cast<long long>(a.tiles_m) * a.tiles_n;
+  const int pairs = pairs_for(a.num_tiles);
+  CUtensorMap ma, mb;
+  if (!encode_i8_map(&ma, xq, a.K, rows, ld_xq, 128)) return AVEY_ERR_CUDA;
+  if (!encode_i8_map(&mb, p->Wq, a.K, a.N, p->ld_w, 128)) return AVEY_ERR_CUDA;
+  const avey_status st = run_linear_pair<256, kScore, false>(ma, mb, ma, ma, a, pairs, s);
+  if (st != AVEY_OK) return st;
+  score_join<<<(rows + 7) / 8, 256, 0, s>>>(a, pairs, xq, ld_xq, p->Wq, p->ld_w, ids, logprob, stats, entropy);
+  AVEY_CHECK_LAUNCH("score_join", s);
+  return AVEY_OK;
+}
+
+}  // namespace
+}  // namespace avey
 
 extern "C" size_t avey_score_tokens_i8_workspace_bytes(int rows, int K, int N) {
   if (rows <= 0 || K <= 0 || N <= 0) return 0;
   return avey_linear_i8_workspace_bytes(AVEY_F32, rows, K) +
-         align256(static_cast<size_t>(score_chunk(rows, N)) * score_ld(N) * 4);
+         std::max(align256(static_cast<size_t>(std::min(rows, kFewRows)) * score_ld(N) * 4),
+                  score_partial_bytes(rows));
 }
 
 extern "C" avey_status avey_score_tokens_i8(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt,
@@ -553,18 +801,14 @@ extern "C" avey_status avey_score_tokens_i8(const avey_linear_i8_params *p, cons
     xq = q;
     xs = sc;
   }
-  float *logits = reinterpret_cast<float *>(static_cast<char *>(ws) +
-                                            avey_linear_i8_workspace_bytes(AVEY_F32, rows, p->K));
+  char *rest = static_cast<char *>(ws) + avey_linear_i8_workspace_bytes(AVEY_F32, rows, p->K);
+  if (rows > kFewRows)
+    return launch_score_i8(p, xq, ld_xq, xs, rows, ids, logprob, stats, entropy,
+                           reinterpret_cast<float4 *>(rest), s);
+  float *logits = reinterpret_cast<float *>(rest);
   const int64_t ld = score_ld(p->N);
-  const int chunk = score_chunk(rows, p->N);
-  for (int r0 = 0; r0 < rows; r0 += chunk) {
-    const int n = std::min(chunk, rows - r0);
-    st = launch_linear_i8(p, xq + r0 * ld_xq, ld_xq, xs + r0, n, nullptr, logits, AVEY_F32, ld, s);
-    if (st != AVEY_OK) return st;
-    st = launch_token_logprobs(logits, AVEY_F32, n, p->N, ld, ids ? ids + r0 : nullptr, 0,
-                               logprob ? logprob + r0 : nullptr, stats ? stats + 2ll * r0 : nullptr,
-                               entropy ? entropy + r0 : nullptr, nullptr, nullptr, s);
-    if (st != AVEY_OK) return st;
-  }
-  return AVEY_OK;
+  st = launch_linear_i8(p, xq, ld_xq, xs, rows, nullptr, logits, AVEY_F32, ld, s);
+  if (st != AVEY_OK) return st;
+  return launch_token_logprobs(logits, AVEY_F32, rows, p->N, ld, ids, 0, logprob, stats, entropy, nullptr,
+                               nullptr, s);
 }

@@ -91,10 +91,15 @@ template <int DT>
 avey_status run_quantize(const void *x, int rows, int cols, long long ld_x, int prenorm, int8_t *q,
                          long long ld_q, float *scale, cudaStream_t s) {
   const int al = quant_rows_aligned(x, DT, rows, ld_x) ? 1 : 0;
-  // one warp holds 1024 values; with fewer rows than SMs a block per row
-  // spreads the loads of a row over eight warps
-  if (cols > kGroups * 256 || rows <= sm_count())
+  // as few warps a row as hold it (1024 values each); with fewer rows than SMs
+  // eight, which spreads the loads of a row
+  constexpr int kHold = kGroups * 256;
+  if (cols > 4 * kHold || rows <= sm_count())
     quantize_rows<DT, 8><<<rows, 256, 0, s>>>(x, rows, cols, ld_x, al, prenorm, q, ld_q, scale);
+  else if (cols > 2 * kHold)
+    quantize_rows<DT, 4><<<(rows + 1) / 2, 256, 0, s>>>(x, rows, cols, ld_x, al, prenorm, q, ld_q, scale);
+  else if (cols > kHold)
+    quantize_rows<DT, 2><<<(rows + 3) / 4, 256, 0, s>>>(x, rows, cols, ld_x, al, prenorm, q, ld_q, scale);
   else
     quantize_rows<DT, 1><<<(rows + 7) / 8, 256, 0, s>>>(x, rows, cols, ld_x, al, prenorm, q, ld_q, scale);
   AVEY_CHECK_LAUNCH("quantize_rows", s);

@@ -103,14 +103,12 @@ struct RowScale {
     inv = 1.0f / s;
   }
 
-  // RNE of the exact x / s.  y = x * inv is off by a few ulp, so rint(y) is
-  // right except next to a half; the remainder r = x - q s is exact in fp32 (a
-  // multiple of half an ulp of s, at most about s / 2), and 2 |r| against s
-  // tells those cases apart.
-  __device__ __forceinline__ int round1(float x) const {
-    float q = rintf(slow ? __fdiv_rn(x, s) : x * inv);
-    const float r = fmaf(-q, s, x);
-    const float r2 = fabsf(r) * 2.0f;
+  // RNE of the exact x / s, tie to even.  The remainder r = x - q s is exact in
+  // fp32 (a multiple of half an ulp of s, at most about s / 2), so 2 |r| against
+  // s tells whether q, off by at most one, is right.
+  __device__ __forceinline__ int exact(float x) const {
+    float q = rintf(__fdiv_rn(x, s));
+    const float r = fmaf(-q, s, x), r2 = fabsf(r) * 2.0f;
     if (r2 >= s) {
       const float o = q + copysignf(1.0f, r);
       if (r2 > s || (static_cast<int>(q) & 1)) q = o;
@@ -118,15 +116,37 @@ struct RowScale {
     return static_cast<int>(fminf(fmaxf(q, -127.0f), 127.0f));
   }
 
+  // Eight values.  x * inv + 1.5 * 2^23 rounds to a whole number whose low byte
+  // is q; inv is off by a few ulp, so q may be wrong next to a half, where
+  // 2 |r| reaches s: then (and for scales whose inverse overflows) all eight
+  // take the exact form.
   __device__ __forceinline__ uint2 quantize8(const float (&v)[8]) const {
     if (zero) return make_uint2(0u, 0u);
+    constexpr float kMagic = 12582912.0f;
+    uint32_t b[8];
+    float far = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float t = fmaf(v[j], inv, kMagic);
+      b[j] = __float_as_uint(t);
+      far = fmaxf(far, fabsf(fmaf(kMagic - t, s, v[j])));
+    }
+    if (slow || far * 2.0f >= s) {
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j) {
+        float x = v[0];
+#pragma unroll
+        for (int q = 1; q < 8; ++q) x = q == j ? v[q] : x;
+        const uint32_t e = static_cast<uint32_t>(exact(x));
+#pragma unroll
+        for (int q = 0; q < 8; ++q) b[q] = q == j ? e : b[q];
+      }
+    }
     uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t a = round1(v[4 * i]) & 0xff, b = round1(v[4 * i + 1]) & 0xff;
-      const uint32_t c = round1(v[4 * i + 2]) & 0xff, d = round1(v[4 * i + 3]) & 0xff;
-      w[i] = a | (b << 8) | (c << 16) | (d << 24);
-    }
+    for (int i = 0; i < 2; ++i)
+      w[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
+                         __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
     return make_uint2(w[0], w[1]);
   }
 };

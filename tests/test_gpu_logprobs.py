@@ -82,7 +82,7 @@ def _check(t, x, ids, top, r):
         np.testing.assert_array_equal(tl[ti < 0], -np.inf)
         tol = ref["tz"][:, None] + U * (np.abs(want + ref["z"][:, None]) + np.abs(want))
         ok = ti >= 0
-        assert (np.abs(tl - want)[ok] <= tol[ok]).all()
+        assert (np.abs(tl[ok] - want[ok]) <= tol[ok]).all()
 
 
 def _ids(rows, V, seed, dev):
