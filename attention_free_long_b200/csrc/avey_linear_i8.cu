@@ -15,10 +15,30 @@ namespace avey {
 namespace {
 
 constexpr int kBK = 128;
-constexpr int kLinEpi = 8, kLinThreads = 64 + 32 * kLinEpi;
+constexpr int kLinEpi = 16, kGroups = kLinEpi / 4, kLinThreads = 64 + 32 * kLinEpi;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar2 = -200.0f;  // ex2 is 0 in fp32 from here down
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// mbar_wait for a whole warp, with one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_suspend(bar, parity))) return true;
+    if ((it & 127u) == 0 &&
+        __any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > kWaitLimitNs))
+      return false;
+  }
+}
 
 // What the epilogue does with the products besides AVEY_F32, AVEY_BF16 and
 // AVEY_BF16X2 (stores): running softmax statistics of each row.
@@ -31,11 +51,12 @@ struct LinLayout {
   static constexpr uint32_t B_BYTES = (BN / 2) * kBK;   // this CTA's half of the channels
   static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr uint32_t BUF = OUT == kScore ? 0 : OUT == AVEY_BF16 ? 2048 : 4096;
-  static constexpr int STAGES = BN < 256 ? 6 : OUT == kScore ? 6 : OUT == AVEY_BF16 ? 5 : 4;
+  static constexpr int BUFS = OUT == AVEY_BF16 ? 2 : 1;
+  static constexpr int STAGES = OUT == kScore ? 6 : BN < 256 ? 6 : 4;
   static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES;
   static constexpr uint32_t CTRL_BYTES = 1024;
   static constexpr uint32_t COLS_BYTES = 2 * 2 * BN * 4;  // scale and bias, two tiles
-  static constexpr uint32_t STAGING_BYTES = kLinEpi * 2 * BUF;
+  static constexpr uint32_t STAGING_BYTES = kLinEpi * BUFS * BUF;
   static constexpr uint32_t SMEM_BYTES = TILES_BYTES + STAGING_BYTES + CTRL_BYTES + COLS_BYTES + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -56,6 +77,29 @@ struct LinArgs {
   long long ld_out;
   float4 *partial;  // kScore: (max, sum, weighted sum) of a row's share of the words
   int *status;
+};
+
+// The tiles first, first + step, .. below end as (row block, column block).
+struct TileWalk {
+  long long tile, end;
+  int mt, nt, step_m, step_n, tiles_n, step;
+  __device__ __forceinline__ TileWalk(const LinArgs &a, long long first, long long end_, long long step_)
+      : tile(first), end(end_), tiles_n(a.tiles_n), step(static_cast<int>(step_)) {
+    mt = static_cast<int>(first / a.tiles_n);
+    nt = static_cast<int>(first - static_cast<long long>(mt) * a.tiles_n);
+    step_m = step / a.tiles_n;
+    step_n = step - step_m * a.tiles_n;
+  }
+  __device__ __forceinline__ bool more() const { return tile < end; }
+  __device__ __forceinline__ void next() {
+    tile += step;
+    mt += step_m;
+    nt += step_n;
+    if (nt >= tiles_n) {
+      nt -= tiles_n;
+      ++mt;
+    }
+  }
 };
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
@@ -264,32 +308,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      long long issued = 0;
-      bool ok = true;
-      for (long long tile = t_first; ok && tile < t_end; tile += t_step) {
-        const int mt = static_cast<int>(tile / a.tiles_n), nt = static_cast<int>(tile % a.tiles_n);
-        const int arow = mt * P::PM + static_cast<int>(rank) * 128;
-        const int brow = nt * BN + static_cast<int>(rank) * (BN / 2);
-        for (int kc = 0; kc < kchunks; ++kc) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
+    // The whole warp walks the loop, so that addresses stay in uniform
+    // registers; one lane issues.
+    const bool one = elect_one();
+    const uint32_t full0 = mapa_shared(full_bar(0), 0);
+    int stage = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    bool ok = true;
+    for (TileWalk w(a, t_first, t_end, t_step); ok && w.more(); w.next()) {
+      const int arow = w.mt * P::PM + static_cast<int>(rank) * 128;
+      const int brow = w.nt * BN + static_cast<int>(rank) * (BN / 2);
+      for (int kc = 0; kc < kchunks; ++kc) {
+        if (!warp_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t st = sbase + stage * P::STAGE_BYTES, bar = full0 + 8u * stage;
+        if (one) {
           if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * P::STAGE_BYTES);
-          const uint32_t full0 = mapa_shared(full_bar(stage), 0);
-          const uint32_t st = sbase + stage * P::STAGE_BYTES;
-          tma_load_3d_pair(st, &tmA, full0, kc * kBK, arow, 0);
-          tma_load_3d_pair(st + P::A_BYTES, &tmB, full0, kc * kBK, brow, 0);
-          ++issued;
-          if (++stage == P::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          tma_load_3d_pair(st, &tmA, bar, kc * kBK, arow, 0);
+          tma_load_3d_pair(st + P::A_BYTES, &tmB, bar, kc * kBK, brow, 0);
+        }
+        ++issued;
+        if (++stage == P::STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
+    }
+    if (one) {
       if (!ok) {
         *abort_flag = 1;
         record_status(a.status, AVEY_ERR_DEVICE_TIMEOUT);
@@ -304,60 +352,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
   } else if (warp == 1) {
     // --------------------------------------------------- MMA issue (CTA 0)
-    if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_s8_s32(P::PM, BN);
+    // Issued from one thread's own loop, a 128-byte K step took about 1000
+    // cycles, twice the tensor time of its four MMAs; warp-uniform code keeps
+    // descriptors in uniform registers.
+    if (rank == 0) {
+      constexpr uint32_t idesc = idesc_s8_s32(P::PM, BN);
+      const bool one = elect_one();
+      const long long tiles = t_first < t_end ? (t_end - t_first + t_step - 1) / t_step : 0;
+      const int last_steps = (a.K - (kchunks - 1) * kBK + 31) / 32;  // MMAs of the last K step; the rest is zeros
+      const uint64_t desc0 = sdesc_k_sw128(sbase);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (long long tile = t_first; ok && tile < t_end; tile += t_step) {
-        if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag)) {
+      for (long long t = 0; ok && t < tiles; ++t) {
+        if (!warp_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
         for (int kc = 0; kc < kchunks; ++kc) {
-          if (!mbar_wait(full_bar(stage), phase, abort_flag)) {
+          if (!warp_wait(full_bar(stage), phase, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t st = sbase + stage * P::STAGE_BYTES;
-          const uint64_t da = sdesc_k_sw128(st), db = sdesc_k_sw128(st + P::A_BYTES);
-          const int steps = min(kBK / 32, (a.K - kc * kBK + 31) / 32);  // the rest is zeros
-          for (int kk = 0; kk < steps; ++kk)
-            tc_mma_i8_pair(d_tmem, da + 2u * kk, db + 2u * kk, idesc, (kc | kk) != 0);
-          tc_commit_pair_both(empty_bar(stage));
+          const uint64_t da = desc0 + static_cast<uint32_t>(stage) * (P::STAGE_BYTES >> 4);
+          const uint64_t db = da + (P::A_BYTES >> 4);
+          const bool whole = kc + 1 < kchunks || last_steps == kBK / 32;
+          if (one) {
+            tc_mma_i8_pair(d_tmem, da, db, idesc, kc != 0);
+            if (whole) {
+#pragma unroll
+              for (int kk = 1; kk < kBK / 32; ++kk) tc_mma_i8_pair(d_tmem, da + 2u * kk, db + 2u * kk, idesc, 1u);
+            } else {
+              for (int kk = 1; kk < last_steps; ++kk)
+                tc_mma_i8_pair(d_tmem, da + 2u * kk, db + 2u * kk, idesc, 1u);
+            }
+            tc_commit_pair_both(empty_bar(stage));
+            if (kc + 1 == kchunks) tc_commit_pair_both(tfull_bar(acc));
+          }
+          __syncwarp();
           if (++stage == P::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (!ok) break;
-        tc_commit_pair_both(tfull_bar(acc));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      if (!ok) {
-        *abort_flag = 1;
-        record_status(a.status, AVEY_ERR_DEVICE_TIMEOUT);
+      if (one) {
+        if (!ok) {
+          *abort_flag = 1;
+          record_status(a.status, AVEY_ERR_DEVICE_TIMEOUT);
+        }
+        tc_commit_pair_both(drain_bar);
+        drain_wait(drain_bar, 0);
       }
-      tc_commit_pair_both(drain_bar);
-      drain_wait(drain_bar, 0);
     }
   } else {
     // ------------------------------------------------------------- epilogue
-    // Eight warps: a quarter of the CTA's rows (TMEM lanes 32*quarter .. +31)
-    // and every other 32-column chunk each.
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const int et = static_cast<int>(threadIdx.x) - 64;  // 0 .. 255
-    const uint32_t stg = sbase + P::TILES_BYTES + static_cast<uint32_t>(warp - 2) * 2u * P::BUF;
+    // Sixteen warps: a quarter of the CTA's rows (TMEM lanes 32*quarter .. +31)
+    // and every fourth 32-column chunk each.  With eight the warps issued in a
+    // third of the cycles only, waiting for TMEM and for one another.
+    const int quarter = warp & 3, group = (warp - 2) >> 2;
+    const int et = static_cast<int>(threadIdx.x) - 64;  // 0 .. 511
+    const uint32_t stg = sbase + P::TILES_BYTES + static_cast<uint32_t>(warp - 2) * P::BUFS * P::BUF;
     const uint32_t tempty_r0 = mapa_shared(tempty_bar(0), 0), tempty_r1 = mapa_shared(tempty_bar(1), 0);
     // scale and bias of this thread's column of a tile; the scores work in
     // units of log 2, and words past the last have the value -inf
-    auto column = [&](long long tile, float &w, float &b) {
-      if (tile >= t_end || et >= BN) return;
-      const int c = static_cast<int>(tile % a.tiles_n) * BN + et;
+    auto column = [&](const TileWalk &at, float &w, float &b) {
+      if (!at.more() || et >= BN) return;
+      const int c = at.nt * BN + et;
       const bool in = c < a.N;
       w = in ? __ldg(a.w_scale + c) : 0.f;
       b = in && a.bias ? __ldg(a.bias + c) : 0.f;
@@ -367,10 +433,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     uint32_t acc_phase = 0;
     bool ok = true;
     float cw = 0.f, cb = 0.f;
-    column(t_first, cw, cb);
+    TileWalk walk(a, t_first, t_end, t_step);
+    column(walk, cw, cb);
     Stat2 st{kLowest, 0.f, 0.f};
-    for (long long tile = t_first; tile < t_end; tile += t_step) {
-      const int mt = static_cast<int>(tile / a.tiles_n), nt = static_cast<int>(tile % a.tiles_n);
+    while (walk.more()) {
+      const int mt = walk.mt, nt = walk.nt;
+      walk.next();  // the tile after this one
       const int row0 = mt * P::PM + static_cast<int>(rank) * 128 + quarter * 32;
       const int row = row0 + lane;
       const bool valid = row < a.rows;
@@ -383,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         w_s[et] = cw;
         b_s[et] = cb;
       }
-      column(tile + t_step, cw, cb);
+      column(walk, cw, cb);
       named_bar_sync(1, 32 * kLinEpi);
       // A warp that gave up still meets the others at the barrier of each tile.
       if (ok && !mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) {
@@ -395,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       const uint32_t taddr =
           tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-      for (int ch = half; ch < BN / 32; ch += 2) {
+      for (int ch = group; ch < BN / 32; ch += kGroups) {
         const int col0 = nt * BN + ch * 32;
         if (col0 >= a.N || row0 >= a.rows) break;  // warp-uniform
         float4 res[RES ? 8 : 1];
@@ -422,9 +490,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           }
           if (col0 + 32 > a.N_tma && valid) store_rest<OUT>(a, row, col0, v);
           if (col0 >= a.N_tma) continue;  // warp-uniform
-          const uint32_t buf = stg + (it & 1) * P::BUF;
-          if (it >= 2) {  // the store issued from this buffer two chunks ago must have read it
-            if (lane == 0) bulk_wait_read<1>();
+          const uint32_t buf = stg + (it % P::BUFS) * P::BUF;
+          if (it >= P::BUFS) {  // the last store issued from this buffer must have read it
+            if (lane == 0) bulk_wait_read<P::BUFS - 1>();
             __syncwarp();
           }
           if constexpr (OUT == AVEY_F32) {
@@ -466,9 +534,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       if constexpr (OUT == kScore) {
         // the row block or the share ends here: pair p meets row block mt in
         // slot p + mt alone, since both only grow along the tiles
-        if (nt == a.tiles_n - 1 || tile + 1 == t_end) {
+        if (nt == a.tiles_n - 1 || !walk.more()) {
           const long long slot = static_cast<long long>(pair) + mt;
-          a.partial[slot * 512 + half * 256 + static_cast<int>(rank) * 128 + quarter * 32 + lane] =
+          a.partial[(slot * kGroups + group) * 256 + static_cast<int>(rank) * 128 + quarter * 32 + lane] =
               make_float4(st.m, st.s, st.t, 0.f);
           st = Stat2{kLowest, 0.f, 0.f};
         }
@@ -670,9 +738,9 @@ __global__ void __launch_bounds__(256)
   while (score_start(p1 + 1, a.num_tiles, npairs) <= last) ++p1;
   while (score_start(p1, a.num_tiles, npairs) > last) --p1;
   Stat2 st{kLowest, 0.f, 0.f};
-  const int parts = 2 * static_cast<int>(p1 - p0 + 1);
+  const int parts = kGroups * static_cast<int>(p1 - p0 + 1);
   for (int i = lane; i < parts; i += 32) {
-    const float4 v = a.partial[(p0 + (i >> 1) + mt) * 512 + (i & 1) * 256 + (row & 255)];
+    const float4 v = a.partial[((p0 + i / kGroups + mt) * kGroups + i % kGroups) * 256 + (row & 255)];
     Stat2 o{v.x, v.y, v.z};
     const float M = fmaxf(st.m, o.m);
     rebase2(st, M);
@@ -727,7 +795,7 @@ constexpr int kFewRows = 32;
 inline int64_t score_ld(int N) { return (static_cast<int64_t>(N) + 7) / 8 * 8; }
 inline size_t score_partial_bytes(int rows) {
   const size_t slots = static_cast<size_t>((rows + 255) / 256) + std::max(1, sm_count() / 2);
-  return slots * 512 * sizeof(float4);
+  return slots * kGroups * 256 * sizeof(float4);
 }
 
 avey_status launch_score_i8(const avey_linear_i8_params *p, const int8_t *xq, int64_t ld_xq,
