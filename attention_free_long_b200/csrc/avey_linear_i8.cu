@@ -19,6 +19,7 @@ constexpr int kLinEpi = 16, kGroups = kLinEpi / 4, kLinThreads = 64 + 32 * kLinE
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar2 = -200.0f;  // ex2 is 0 in fp32 from here down
+constexpr float kMaskedWord = -1e30f;
 
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -55,7 +56,7 @@ struct LinLayout {
   static constexpr int STAGES = OUT == kScore ? 6 : BN < 256 ? 6 : 4;
   static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES;
   static constexpr uint32_t CTRL_BYTES = 1024;
-  static constexpr uint32_t COLS_BYTES = 2 * 2 * BN * 4;  // scale and bias, two tiles
+  static constexpr uint32_t COLS_BYTES = kLinEpi * 2 * 32 * 4;  // each warp's scale and bias
   static constexpr uint32_t STAGING_BYTES = kLinEpi * BUFS * BUF;
   static constexpr uint32_t SMEM_BYTES = TILES_BYTES + STAGING_BYTES + CTRL_BYTES + COLS_BYTES + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
@@ -234,8 +235,6 @@ __device__ __forceinline__ void score_values(float (&v)[32], float xs, const flo
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     float2 d = fadd2(make_float2(v[2 * j], v[2 * j + 1]), minus);
-    d.x = max_nan(d.x, kFar2);
-    d.y = max_nan(d.y, kFar2);
     const float2 e = make_float2(ex2(d.x), ex2(d.y));
     s = fadd2(s, e);
     t = ffma2(e, d, t);
@@ -256,7 +255,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   uint8_t *ctrl = smem_raw + pad + P::TILES_BYTES + P::STAGING_BYTES;
   const uint32_t sbase = raw_s + pad;
   const uint32_t cbase = sbase + P::TILES_BYTES + P::STAGING_BYTES;
-  float *cols = reinterpret_cast<float *>(ctrl + P::CTRL_BYTES);  // [2 tiles][scale, bias][BN]
   // control block: full[8] @0, empty[8] @64, tfull[2] @128, tempty[2] @144,
   // drain @160, tmem base @168, abort flag @172
   auto full_bar = [&](int s) { return cbase + 8u * s; };
@@ -416,25 +414,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     // and every fourth 32-column chunk each.  With eight the warps issued in a
     // third of the cycles only, waiting for TMEM and for one another.
     const int quarter = warp & 3, group = (warp - 2) >> 2;
-    const int et = static_cast<int>(threadIdx.x) - 64;  // 0 .. 511
     const uint32_t stg = sbase + P::TILES_BYTES + static_cast<uint32_t>(warp - 2) * P::BUFS * P::BUF;
     const uint32_t tempty_r0 = mapa_shared(tempty_bar(0), 0), tempty_r1 = mapa_shared(tempty_bar(1), 0);
-    // scale and bias of this thread's column of a tile; the scores work in
-    // units of log 2, and words past the last have the value -inf
-    auto column = [&](const TileWalk &at, float &w, float &b) {
-      if (!at.more() || et >= BN) return;
-      const int c = at.nt * BN + et;
+    float *w_s = reinterpret_cast<float *>(ctrl + P::CTRL_BYTES) + (warp - 2) * 64, *b_s = w_s + 32;
+    // Scale and bias of this lane's column of a chunk, fetched a chunk ahead.
+    // The scores work in units of log 2, where words past the last have the
+    // value -1e30, as those with a bias below it (-inf among them): finite, so
+    // that 0 * (y - m) stays 0.
+    float cw = 0.f, cb = 0.f;
+    auto column = [&](int nt, int ch) {
+      const int c = nt * BN + ch * 32 + lane;
       const bool in = c < a.N;
-      w = in ? __ldg(a.w_scale + c) : 0.f;
-      b = in && a.bias ? __ldg(a.bias + c) : 0.f;
-      if constexpr (OUT == kScore) b = in ? b * kLog2e : -INFINITY;
+      cw = in ? __ldg(a.w_scale + c) : 0.f;
+      cb = in && a.bias ? __ldg(a.bias + c) : 0.f;
+      if constexpr (OUT == kScore) cb = in ? max_nan(cb * kLog2e, kMaskedWord) : kMaskedWord;
+    };
+    auto row_scale = [&](int mt) {
+      const int row = mt * P::PM + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+      return row < a.rows ? __ldg(a.x_scale + row) * (OUT == kScore ? kLog2e : 1.f) : 0.f;
     };
     int acc = 0, it = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    float cw = 0.f, cb = 0.f;
     TileWalk walk(a, t_first, t_end, t_step);
-    column(walk, cw, cb);
+    float xs_next = 0.f;
+    if (walk.more()) {
+      column(walk.nt, group);
+      xs_next = row_scale(walk.mt);
+    }
     Stat2 st{kLowest, 0.f, 0.f};
     while (walk.more()) {
       const int mt = walk.mt, nt = walk.nt;
@@ -442,30 +449,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       const int row0 = mt * P::PM + static_cast<int>(rank) * 128 + quarter * 32;
       const int row = row0 + lane;
       const bool valid = row < a.rows;
-      float xs = valid ? __ldg(a.x_scale + row) : 0.f;
-      if constexpr (OUT == kScore) xs *= kLog2e;
-      // Columns of tile i go to buffer i & 1.  A warp here has passed the barrier
-      // of tile i - 1, so every warp is done with tile i - 2, the buffer's last.
-      float *w_s = cols + acc * 2 * BN, *b_s = w_s + BN;
-      if (et < BN) {
-        w_s[et] = cw;
-        b_s[et] = cb;
-      }
-      column(walk, cw, cb);
-      named_bar_sync(1, 32 * kLinEpi);
-      // A warp that gave up still meets the others at the barrier of each tile.
-      if (ok && !mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) {
+      const float xs = xs_next;
+      if (walk.more() && walk.mt != mt) xs_next = row_scale(walk.mt);
+      if (!warp_wait(tfull_bar(acc), acc_phase, abort_flag)) {
         ok = false;
-        *abort_flag = 1;
+        break;
       }
-      if (!ok) continue;
       tc_fence_after();
       const uint32_t taddr =
           tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
       for (int ch = group; ch < BN / 32; ch += kGroups) {
         const int col0 = nt * BN + ch * 32;
-        if (col0 >= a.N || row0 >= a.rows) break;  // warp-uniform
+        if (col0 >= a.N || row0 >= a.rows) {  // warp-uniform; the chunk fetched ahead is another one
+          if (walk.more()) column(walk.nt, group);
+          break;
+        }
+        w_s[lane] = cw;
+        b_s[lane] = cb;
+        __syncwarp();
+        if (ch + kGroups < BN / 32)
+          column(nt, ch + kGroups);
+        else if (walk.more())
+          column(walk.nt, group);
         float4 res[RES ? 8 : 1];
         if constexpr (RES) {
           const float *rr = a.residual + static_cast<long long>(row) * a.ld_out;
@@ -476,9 +482,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         float v[32];
         tmem_ld32(taddr + ch * 32, v);
         if constexpr (OUT == kScore) {
-          score_values(v, xs, w_s + ch * 32, b_s + ch * 32, st);
+          score_values(v, xs, w_s, b_s, st);
+          __syncwarp();
         } else {
-          lin_values(v, xs, w_s + ch * 32, b_s + ch * 32, a.relu2);
+          lin_values(v, xs, w_s, b_s, a.relu2);
+          __syncwarp();
           if constexpr (RES) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -770,7 +778,7 @@ __global__ void __launch_bounds__(256)
     acc += __shfl_xor_sync(0xffffffffu, acc, off);
   }
   if (lane != 0) return;
-  const bool empty = st.s == 0.f;
+  const bool empty = st.m <= 0.5f * kMaskedWord;
   const bool bad = !(st.s < INFINITY) || st.m == INFINITY;
   const float nan = __uint_as_float(0x7fc00000u);
   const float z = logf(st.s);

@@ -465,7 +465,8 @@ AVEY_API avey_status avey_token_logprobs_backward(const void *logits, avey_dtype
 /* avey_score_tokens_i8: avey_linear_i8 against a vocabulary matrix (p->N words,
  * act AVEY_ACT_NONE), then logprob, stats and entropy of its rows as
  * avey_token_logprobs defines them, on logits that are not rounded below fp32
- * and not an output.  x, x_dt, ld_x, x_scale, prenorm as avey_linear_i8;
+ * and not an output.  A bias below -1e29 counts as -inf; a logit that overflows
+ * fp32 makes its row NaN.  x, x_dt, ld_x, x_scale, prenorm as avey_linear_i8;
  * outputs as avey_token_logprobs (any may be NULL, not all).
  * ws: at least avey_score_tokens_i8_workspace_bytes(...) bytes, 256-byte
  * aligned. */
