@@ -22,7 +22,6 @@ same forward after the ranker, for a selection the caller supplies.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -356,17 +355,26 @@ def avey_static_mix(V: torch.Tensor, zt: torch.Tensor, S: int, mt: Optional[int]
 
 # --------------------------------------------------- 8-bit products, scoring --
 
-_here = contextlib.nullcontext()
+def _call(fn: str, t: torch.Tensor, *args) -> None:
+    """Calls the library on the current stream of t's device, the last argument."""
+    dev = t.get_device()
+    if dev == torch._C._cuda_getDevice():
+        code = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if code:
+        _check(fn, code)
 
 
-def _on(t: torch.Tensor):
-    """Makes t's device current, so that the call runs on its current stream."""
-    return _here if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _same_device(t: torch.Tensor, *others) -> None:
+    dev = t.get_device()
     for o in others:
-        if o is not None and o.device != t.device:
+        if o is not None and o.get_device() != dev:
             raise ValueError(f"tensors on {t.device} and {o.device} in one call")
 
 
@@ -375,8 +383,10 @@ def _rows_of(t: torch.Tensor, name: str):
     if not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a CUDA matrix")
     rows, cols = t.shape
-    ld = t.stride(0) if rows > 1 else cols
-    if cols < 1 or (cols > 1 and t.stride(1) != 1) or ld < cols:
+    ld, step = t.stride()
+    if rows <= 1:
+        ld = cols
+    if cols < 1 or (cols > 1 and step != 1) or ld < cols:
         raise ValueError(f"{name} must have contiguous, non-overlapping rows of at least one column")
     return rows, cols, ld
 
@@ -384,8 +394,9 @@ def _rows_of(t: torch.Tensor, name: str):
 def _vector(t: Optional[torch.Tensor], name: str, n: int, dtype: torch.dtype) -> None:
     if t is None:
         return
-    _need(t, name)
-    if t.dtype != dtype or t.shape != (n,):
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n:
         raise TypeError(f"{name} must be {dtype} [{n}]")
 
 
@@ -408,7 +419,7 @@ class QuantRows:
     cols: int
 
 
-@dataclass
+@dataclass(frozen=True)
 class QuantLinear:
     """Weights of an 8-bit product: channel n is scale[n] * q[n, :K]."""
     q: torch.Tensor  # int8 [N, ld], ld a multiple of 16
@@ -436,11 +447,10 @@ def avey_quantize_rows(x: torch.Tensor, prenorm: bool = False) -> QuantRows:
     [2, rows, cols]) as 8-bit integers with a scale per row; prenorm: of the
     RMS-normalised rows."""
     dt, rows, cols, ld = _quant_source(x)
-    q = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=x.device)
-    scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    with _on(x):
-        _check("avey_quantize_rows", lib().avey_quantize_rows(
-            _ptr(x), dt, rows, cols, ld, int(bool(prenorm)), _ptr(q), q.shape[1], _ptr(scale), _stream()))
+    q = x.new_empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8)
+    scale = x.new_empty((rows,), dtype=torch.float32)
+    _call("avey_quantize_rows", x, x.data_ptr(), dt, rows, cols, ld, 1 if prenorm else 0, q.data_ptr(),
+          q.shape[1], scale.data_ptr())
     return QuantRows(q, scale, cols)
 
 
@@ -467,6 +477,17 @@ def _linear_input(x, lin: QuantLinear):
     return t, dt, rows, ld, scale
 
 
+def _scratch(ws: Optional[torch.Tensor], need: int, t: torch.Tensor):
+    """(workspace, bytes): ws when it is large enough, else a new one; None for 0."""
+    if need == 0:
+        return None, 0
+    if ws is None or ws.numel() < need:
+        ws = t.new_empty((need,), dtype=torch.uint8)
+    elif not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
+        raise ValueError("ws must be a contiguous CUDA uint8 tensor")
+    return ws, ws.numel()
+
+
 def avey_linear_i8(x, lin: QuantLinear, act: int = AVEY_ACT_NONE,
                    residual: Optional[torch.Tensor] = None, prenorm: bool = False,
                    out_dtype: torch.dtype = torch.float32, pair: bool = False,
@@ -485,8 +506,10 @@ def avey_linear_i8(x, lin: QuantLinear, act: int = AVEY_ACT_NONE,
     N = lin.q.shape[0]
     if out is None:
         ld_out = (N + 7) // 8 * 8
-        shape = (2, rows, ld_out) if pair else (rows, ld_out)
-        out = torch.empty(shape, dtype=torch.bfloat16 if pair else out_dtype, device=t.device)
+        if pair:
+            out = t.new_empty((2, rows, ld_out), dtype=torch.bfloat16)
+        else:
+            out = t.new_empty((rows, ld_out), dtype=out_dtype)
         if ld_out != N:
             out = out[..., :N]
     elif pair:
@@ -506,19 +529,15 @@ def avey_linear_i8(x, lin: QuantLinear, act: int = AVEY_ACT_NONE,
         if residual.dtype != torch.float32 or (r, c) != (rows, N):
             raise TypeError(f"residual must be fp32 [{rows}, {N}]")
         if (rows > 1 and ld_r != ld_out) or residual.data_ptr() % 16:
-            padded = torch.empty((rows, ld_out), dtype=torch.float32, device=t.device)
+            _same_device(t, residual)
+            padded = t.new_empty((rows, ld_out), dtype=torch.float32)
             padded[:, :N].copy_(residual)
             residual = padded
     _same_device(t, out, residual, ws)
-    L = lib()
-    with _on(t):
-        need = 0 if dt == AVEY_I8 else int(L.avey_linear_i8_workspace_bytes(dt, rows, lin.K))
-        if need and (ws is None or ws.numel() < need):
-            ws = _ws(need, t.device)
-        p = lin._params(act)
-        _check("avey_linear_i8", L.avey_linear_i8(
-            ctypes.byref(p), _ptr(t), dt, ld, _ptr(scale), int(bool(prenorm)), rows, _ptr(residual),
-            _ptr(out), out_dt, ld_out, _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
+    need = 0 if dt == AVEY_I8 else lib().avey_linear_i8_workspace_bytes(dt, rows, lin.K)
+    ws, ws_bytes = _scratch(ws, need, t)
+    _call("avey_linear_i8", t, ctypes.byref(lin._params(act)), t.data_ptr(), dt, ld, _addr(scale),
+          1 if prenorm else 0, rows, _addr(residual), out.data_ptr(), out_dt, ld_out, _addr(ws), ws_bytes)
     return out
 
 
@@ -544,16 +563,16 @@ def avey_token_logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None
     dt = _dt(logits)
     _vector(ids, "ids", rows, torch.int32)
     _same_device(logits, ids)
-    f = lambda *s: torch.empty(s, dtype=torch.float32, device=logits.device)
-    logprob = None if ids is None else f(rows)
-    stats, entropy = f(rows, 2), f(rows)
-    top_ids = top_lp = None
+    f32 = torch.float32
+    stats, entropy = logits.new_empty((rows, 2), dtype=f32), logits.new_empty((rows,), dtype=f32)
+    logprob = top_ids = top_lp = None
+    if ids is not None:
+        logprob = logits.new_empty((rows,), dtype=f32)
     if top > 0:
-        top_ids, top_lp = torch.empty((rows, top), dtype=torch.int32, device=logits.device), f(rows, top)
-    with _on(logits):
-        _check("avey_token_logprobs", lib().avey_token_logprobs(
-            _ptr(logits), dt, rows, V, ld, _ptr(ids), top, _ptr(logprob), _ptr(stats), _ptr(entropy),
-            _ptr(top_ids), _ptr(top_lp), _stream()))
+        top_ids = logits.new_empty((rows, top), dtype=torch.int32)
+        top_lp = logits.new_empty((rows, top), dtype=f32)
+    _call("avey_token_logprobs", logits, logits.data_ptr(), dt, rows, V, ld, _addr(ids), top, _addr(logprob),
+          stats.data_ptr(), entropy.data_ptr(), _addr(top_ids), _addr(top_lp))
     return TokenLogprobs(logprob, stats, entropy, top_ids, top_lp)
 
 
@@ -574,15 +593,15 @@ def avey_token_logprobs_backward(logits: torch.Tensor, ids: Optional[torch.Tenso
     if scores.stats.dtype != torch.float32 or scores.stats.shape != (rows, 2):
         raise TypeError(f"stats must be fp32 [{rows}, 2]")
     if out is None:
-        out = torch.empty((rows, V), dtype=logits.dtype, device=logits.device)
-    r, c, ld_d = _rows_of(out, "out")
-    if (r, c) != (rows, V) or out.dtype != logits.dtype:
-        raise TypeError(f"out must be {logits.dtype} [{rows}, {V}]")
+        out, ld_d = logits.new_empty((rows, V)), V
+    else:
+        r, c, ld_d = _rows_of(out, "out")
+        if (r, c) != (rows, V) or out.dtype != logits.dtype:
+            raise TypeError(f"out must be {logits.dtype} [{rows}, {V}]")
     _same_device(logits, ids, scores.stats, scores.entropy, d_logprob, d_entropy, out)
-    with _on(logits):
-        _check("avey_token_logprobs_backward", lib().avey_token_logprobs_backward(
-            _ptr(logits), dt, rows, V, ld, _ptr(ids), _ptr(scores.stats), _ptr(scores.entropy),
-            _ptr(d_logprob), _ptr(d_entropy), _ptr(out), ld_d, _stream()))
+    _call("avey_token_logprobs_backward", logits, logits.data_ptr(), dt, rows, V, ld, _addr(ids),
+          scores.stats.data_ptr(), scores.entropy.data_ptr(), _addr(d_logprob), _addr(d_entropy),
+          out.data_ptr(), ld_d)
     return out
 
 
@@ -600,18 +619,14 @@ def avey_score_tokens_i8(x, head: QuantLinear, ids: Optional[torch.Tensor] = Non
     t, dt, rows, ld, scale = _linear_input(x, head)
     _vector(ids, "ids", rows, torch.int32)
     _same_device(t, ids, ws)
-    f = lambda *s: torch.empty(s, dtype=torch.float32, device=t.device)
-    logprob = None if ids is None else f(rows)
-    stats, entropy = f(rows, 2), f(rows)
-    L = lib()
-    with _on(t):
-        need = int(L.avey_score_tokens_i8_workspace_bytes(rows, head.K, head.q.shape[0]))
-        if need and (ws is None or ws.numel() < need):
-            ws = _ws(need, t.device)
-        p = head._params(AVEY_ACT_NONE)
-        _check("avey_score_tokens_i8", L.avey_score_tokens_i8(
-            ctypes.byref(p), _ptr(t), dt, ld, _ptr(scale), int(bool(prenorm)), rows, _ptr(ids),
-            _ptr(logprob), _ptr(stats), _ptr(entropy), _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
+    f32 = torch.float32
+    logprob = None if ids is None else t.new_empty((rows,), dtype=f32)
+    stats, entropy = t.new_empty((rows, 2), dtype=f32), t.new_empty((rows,), dtype=f32)
+    need = lib().avey_score_tokens_i8_workspace_bytes(rows, head.K, head.q.shape[0])
+    ws, ws_bytes = _scratch(ws, need, t)
+    _call("avey_score_tokens_i8", t, ctypes.byref(head._params(AVEY_ACT_NONE)), t.data_ptr(), dt, ld,
+          _addr(scale), 1 if prenorm else 0, rows, _addr(ids), _addr(logprob), stats.data_ptr(),
+          entropy.data_ptr(), _addr(ws), ws_bytes)
     return TokenLogprobs(logprob, stats, entropy)
 
 

@@ -1,0 +1,276 @@
+// avey_linear_few.cu -- the 8-bit product for up to 32 rows (single tokens of a
+// decoder or a head): bound by one read of the weights, and by latency.
+//
+// A warp owns 16 output channels and walks K in steps of 64: mma.sync m16n8k32
+// with the weights as A straight from global memory and eight tokens as B from
+// shared memory.  A sum does not care about the order of its terms, so both
+// operands use the order that suits the loads: lane 4 g + q takes the 16 bytes
+// k = 16 q .. 16 q + 15 of its channels (g and g + 8) and of token g, and two
+// MMAs eat them as "columns" 4 q .. and 16 + 4 q ..  A warp's loads cover whole
+// 64-byte pieces of 16 rows; rows are prefetched into L2 before the block
+// prepares its tokens.  Up to 16 rows are quantised by every block for itself
+// (a few KB from L2), which saves the launch of the rounding kernel.
+// 128-row tiles of tcgen05 would spend the same reads on rows that are not
+// there: one token against 50368 x 768 weights took 22 us that way.
+#include <algorithm>
+
+#include "avey_common.cuh"
+#include "avey_internal.h"
+#include "avey_quant.cuh"
+
+namespace avey {
+namespace {
+
+struct FewArgs {
+  const void *x;
+  long long ld_x;
+  int x_aligned, prenorm;
+  const float *x_scale;
+  int rows, N, K, stride;  // stride: bytes of a token in shared memory
+  const int8_t *Wq;
+  long long ld_w;
+  const float *w_scale, *bias, *residual;
+  int relu2;
+  void *out;
+  long long ld_out;
+};
+
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                       uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// One row of x as 8-bit integers into shared memory (zeros behind K), by a warp.
+template <int DT>
+__device__ __forceinline__ void quantize_row_to(const FewArgs &a, int row, int8_t *dst, float *scale, int lane) {
+  const QuantSource<DT> src(a.x, row, a.rows, a.K, a.ld_x, a.x_aligned);
+  constexpr int kHold = 4;
+  const int groups = a.stride / 8;
+  float v[kHold][8];
+  uint32_t mx = 0;
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) {
+    if (lane + 32 * i < groups) {
+      src.load(lane + 32 * i, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) quant_scan(v[i], mx, ss);
+  for (int g = lane + 32 * kHold; g < groups; g += 32) {
+    float t[8];
+    src.load(g, t);
+    quant_scan(t, mx, ss);
+  }
+  mx = __reduce_max_sync(0xffffffffu, mx);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  const RowScale rs(mx);
+  if (lane == 0)
+    *scale = a.prenorm ? rs.scale * (1.0f / sqrtf(ss / static_cast<float>(a.K) + 1e-6f)) : rs.scale;
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (lane + 32 * i < groups) *reinterpret_cast<uint2 *>(dst + (lane + 32 * i) * 8) = rs.quantize8(v[i]);
+  for (int g = lane + 32 * kHold; g < groups; g += 32) {
+    float t[8];
+    src.load(g, t);
+    *reinterpret_cast<uint2 *>(dst + g * 8) = rs.quantize8(t);
+  }
+}
+
+// NB blocks of eight tokens, WARPS x 16 channels a block, DT the type of x.
+template <int NB, int WARPS, int DT, int OUT>
+__global__ void __launch_bounds__(WARPS * 32) linear_i8_few(const FewArgs a) {
+  extern __shared__ __align__(16) int8_t xs_q[];
+  __shared__ float xs[NB * 8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q = lane & 3;
+  const int n0 = (blockIdx.x * WARPS + warp) * 16;
+  const int k16 = (a.K + 15) / 16 * 16;  // bytes of a weight row that may be read
+  {
+    const int lines = (k16 + 127) / 128;
+    for (int i = lane; i < 16 * lines; i += 32) {
+      const int n = n0 + i / lines;
+      if (n < a.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.Wq + n * a.ld_w + (i % lines) * 128));
+    }
+  }
+  for (int t = warp; t < NB * 8; t += WARPS) {
+    int8_t *dst = xs_q + t * a.stride;
+    if (t >= a.rows) {
+      for (int i = lane * 8; i < a.stride; i += 256) *reinterpret_cast<uint2 *>(dst + i) = make_uint2(0, 0);
+      if (lane == 0) xs[t] = 0.f;
+    } else if constexpr (DT == AVEY_I8) {
+      const int8_t *src = static_cast<const int8_t *>(a.x) + t * a.ld_x;
+      for (int i = lane * 16; i < a.stride; i += 512) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (i < k16) w = *reinterpret_cast<const uint4 *>(src + i);
+        if (i < a.K && i + 16 > a.K) {  // bytes behind K are not ours
+          uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int keep = a.K - i - 4 * j;
+            v[j] = keep >= 4 ? v[j] : keep <= 0 ? 0u : v[j] & (0xffffffffu >> (32 - 8 * keep));
+          }
+          w = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        *reinterpret_cast<uint4 *>(dst + i) = w;
+      }
+      if (lane == 0) xs[t] = a.x_scale[t];
+    } else {
+      quantize_row_to<DT>(a, t, dst, xs + t, lane);
+    }
+  }
+  __syncthreads();
+  if (n0 >= a.N) return;
+
+  int acc[NB][4] = {};
+  const int8_t *w0 = a.Wq + static_cast<long long>(min(n0 + g, a.N - 1)) * a.ld_w + q * 16;
+  const int8_t *w1 = a.Wq + static_cast<long long>(min(n0 + g + 8, a.N - 1)) * a.ld_w + q * 16;
+  const int8_t *xrow = xs_q + g * a.stride + q * 16;
+  constexpr int UN = 4;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int k0 = 0; k0 < k16; k0 += 64 * UN) {
+    uint4 u[UN], v[UN];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int k = k0 + 64 * i;
+      const bool in = k + q * 16 < k16;
+      u[i] = in ? __ldg(reinterpret_cast<const uint4 *>(w0 + k)) : zero;
+      v[i] = in ? __ldg(reinterpret_cast<const uint4 *>(w1 + k)) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int k = k0 + 64 * i;
+      if (k >= k16) break;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(xrow + b * 8 * a.stride + k);
+        mma_s8(acc[b], u[i].x, v[i].x, u[i].y, v[i].y, x.x, x.y);
+        mma_s8(acc[b], u[i].z, v[i].z, u[i].w, v[i].w, x.z, x.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = n0 + g + 8 * h;
+    if (n >= a.N) continue;
+    const float w = __ldg(a.w_scale + n), bias = a.bias ? __ldg(a.bias + n) : 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = b * 8 + 2 * q + e;
+        if (t >= a.rows) continue;
+        float y = fmaf(static_cast<float>(acc[b][2 * h + e]) * xs[t], w, bias);
+        if (a.relu2) {
+          y = y < 0.f ? 0.f : y;  // NaN stays NaN
+          y *= y;
+        }
+        const long long at = t * a.ld_out + n;
+        if constexpr (OUT == AVEY_F32) {
+          if (a.residual) y += a.residual[at];
+          static_cast<float *>(a.out)[at] = y;
+        } else {
+          bf16 *hi = static_cast<bf16 *>(a.out) + at;
+          *hi = __float2bfloat16_rn(y);
+          if constexpr (OUT == AVEY_BF16X2) {
+            float vh, vl;
+            split_bf16(y, vh, vl);
+            hi[a.rows * a.ld_out] = __float2bfloat16_rn(vl);
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int NB, int WARPS, int DT, int OUT>
+avey_status run_few(const FewArgs &a, cudaStream_t s) {
+  auto kern = linear_i8_few<NB, WARPS, DT, OUT>;
+  const int bytes = NB * 8 * a.stride;
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      set_detail("linear_i8_few: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      return AVEY_ERR_CUDA;
+    }
+  }
+  kern<<<(a.N + 16 * WARPS - 1) / (16 * WARPS), WARPS * 32, bytes, s>>>(a);
+  AVEY_CHECK_LAUNCH("linear_i8_few", s);
+  return AVEY_OK;
+}
+
+template <int NB, int DT, int OUT>
+avey_status run_few_warps(const FewArgs &a, cudaStream_t s) {
+  // four warps a block while that leaves SMs without one; eight share the
+  // preparation of the tokens among more channels
+  if (a.N <= 64 * sm_count()) return run_few<NB, 4, DT, OUT>(a, s);
+  return run_few<NB, 8, DT, OUT>(a, s);
+}
+
+template <int NB, int DT>
+avey_status run_few_out(const FewArgs &a, avey_dtype out_dt, cudaStream_t s) {
+  if (out_dt == AVEY_F32) return run_few_warps<NB, DT, AVEY_F32>(a, s);
+  if (out_dt == AVEY_BF16) return run_few_warps<NB, DT, AVEY_BF16>(a, s);
+  return run_few_warps<NB, DT, AVEY_BF16X2>(a, s);
+}
+
+constexpr int kFewShared = 96 * 1024;  // at most two blocks' worth of an SM
+
+inline int few_stride(int K) { return (K + 127) / 128 * 128 + 64; }  // odd multiples of 64: no bank conflicts
+inline int few_blocks(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+}  // namespace
+
+bool linear_few_fits(int rows, int K) {
+  return rows <= 32 && static_cast<long long>(few_blocks(rows)) * 8 * few_stride(K) <= kFewShared;
+}
+
+bool linear_few_quantizes(avey_dtype x_dt, int rows, int K) {
+  return x_dt != AVEY_I8 && rows <= 16 && linear_few_fits(rows, K);
+}
+
+avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt, int64_t ld_x,
+                              const float *x_scale, int prenorm, int rows, const float *residual,
+                              void *out, avey_dtype out_dt, int64_t ld_out, cudaStream_t s) {
+  FewArgs a{};
+  a.x = x;
+  a.ld_x = ld_x;
+  a.x_aligned = x_dt != AVEY_I8 && quant_rows_aligned(x, x_dt, rows, ld_x);
+  a.prenorm = prenorm;
+  a.x_scale = x_scale;
+  a.rows = rows;
+  a.N = p->N;
+  a.K = p->K;
+  a.stride = few_stride(p->K);
+  a.Wq = p->Wq;
+  a.ld_w = p->ld_w;
+  a.w_scale = p->w_scale;
+  a.bias = p->bias;
+  a.residual = residual;
+  a.relu2 = p->act == AVEY_ACT_RELU2;
+  a.out = out;
+  a.ld_out = ld_out;
+  const int nb = few_blocks(rows);
+#define AVEY_FEW(DT)                                        \
+  return nb == 1 ? run_few_out<1, DT>(a, out_dt, s) : run_few_out<2, DT>(a, out_dt, s)
+  switch (x_dt) {
+    case AVEY_F32: AVEY_FEW(AVEY_F32);
+    case AVEY_BF16: AVEY_FEW(AVEY_BF16);
+    case AVEY_BF16X2: AVEY_FEW(AVEY_BF16X2);
+    default:
+      if (nb == 4) return run_few_out<4, AVEY_I8>(a, out_dt, s);
+      AVEY_FEW(AVEY_I8);
+  }
+#undef AVEY_FEW
+}
+
+}  // namespace avey

@@ -627,6 +627,8 @@ avey_status launch_linear_i8(const avey_linear_i8_params *p, const int8_t *xq, i
                              const float *x_scale, int rows, const float *residual, void *out,
                              avey_dtype out_dt, int64_t ld_out, cudaStream_t s) {
   if (rows == 0) return AVEY_OK;
+  if (linear_few_fits(rows, p->K))
+    return launch_linear_few(p, xq, AVEY_I8, ld_xq, x_scale, 0, rows, residual, out, out_dt, ld_out, s);
   LinArgs a{};
   a.rows = rows;
   a.N = p->N;
@@ -680,9 +682,24 @@ avey_status check_linear_i8(const char *fn, const avey_linear_i8_params *p, cons
 
 using namespace avey;
 
-extern "C" size_t avey_linear_i8_workspace_bytes(avey_dtype x_dt, int rows, int K) {
-  if (x_dt == AVEY_I8 || rows <= 0 || K <= 0) return 0;
+// x as 8-bit rows at the start of the workspace.
+static size_t quantized_bytes(int rows, int K) {
   return align256(static_cast<size_t>(rows) * round16(K)) + align256(static_cast<size_t>(rows) * 4);
+}
+static avey_status quantize_to_ws(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt, int64_t ld_x,
+                                  int prenorm, int rows, void *ws, const int8_t **xq, int64_t *ld_xq,
+                                  const float **xs, cudaStream_t s) {
+  *ld_xq = round16(p->K);
+  int8_t *q = static_cast<int8_t *>(ws);
+  float *sc = reinterpret_cast<float *>(q + align256(static_cast<size_t>(rows) * *ld_xq));
+  *xq = q;
+  *xs = sc;
+  return launch_quantize_rows(x, x_dt, rows, p->K, ld_x, prenorm ? 1 : 0, q, *ld_xq, sc, s);
+}
+
+extern "C" size_t avey_linear_i8_workspace_bytes(avey_dtype x_dt, int rows, int K) {
+  if (x_dt == AVEY_I8 || rows <= 0 || K <= 0 || linear_few_quantizes(x_dt, rows, K)) return 0;
+  return quantized_bytes(rows, K);
 }
 
 extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt,
@@ -709,17 +726,14 @@ extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void
   AVEY_REQUIRE(ws_bytes >= need, AVEY_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu required", fn, ws_bytes,
                need);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (linear_few_quantizes(x_dt, rows, p->K))
+    return launch_linear_few(p, x, x_dt, ld_x, nullptr, prenorm ? 1 : 0, rows, residual, out, out_dt, ld_out, s);
   const int8_t *xq = static_cast<const int8_t *>(x);
   const float *xs = x_scale;
   int64_t ld_xq = ld_x;
   if (x_dt != AVEY_I8) {
-    ld_xq = round16(p->K);
-    int8_t *q = static_cast<int8_t *>(ws);
-    float *sc = reinterpret_cast<float *>(q + align256(static_cast<size_t>(rows) * ld_xq));
-    st = launch_quantize_rows(x, x_dt, rows, p->K, ld_x, prenorm ? 1 : 0, q, ld_xq, sc, s);
+    st = quantize_to_ws(p, x, x_dt, ld_x, prenorm, rows, ws, &xq, &ld_xq, &xs, s);
     if (st != AVEY_OK) return st;
-    xq = q;
-    xs = sc;
   }
   return launch_linear_i8(p, xq, ld_xq, xs, rows, residual, out, out_dt, ld_out, s);
 }
@@ -837,7 +851,7 @@ avey_status launch_score_i8(const avey_linear_i8_params *p, const int8_t *xq, in
 
 extern "C" size_t avey_score_tokens_i8_workspace_bytes(int rows, int K, int N) {
   if (rows <= 0 || K <= 0 || N <= 0) return 0;
-  return avey_linear_i8_workspace_bytes(AVEY_F32, rows, K) +
+  return quantized_bytes(rows, K) +
          std::max(align256(static_cast<size_t>(std::min(rows, kFewRows)) * score_ld(N) * 4),
                   score_partial_bytes(rows));
 }
@@ -865,25 +879,24 @@ extern "C" avey_status avey_score_tokens_i8(const avey_linear_i8_params *p, cons
   AVEY_REQUIRE(ws_bytes >= need, AVEY_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu required", fn, ws_bytes,
                need);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int8_t *xq = static_cast<const int8_t *>(x);
-  const float *xs = x_scale;
-  int64_t ld_xq = ld_x;
-  if (x_dt != AVEY_I8) {
-    ld_xq = round16(p->K);
-    int8_t *q = static_cast<int8_t *>(ws);
-    float *sc = reinterpret_cast<float *>(q + align256(static_cast<size_t>(rows) * ld_xq));
-    st = launch_quantize_rows(x, x_dt, rows, p->K, ld_x, prenorm ? 1 : 0, q, ld_xq, sc, s);
-    if (st != AVEY_OK) return st;
-    xq = q;
-    xs = sc;
-  }
-  char *rest = static_cast<char *>(ws) + avey_linear_i8_workspace_bytes(AVEY_F32, rows, p->K);
-  if (rows > kFewRows)
-    return launch_score_i8(p, xq, ld_xq, xs, rows, ids, logprob, stats, entropy,
-                           reinterpret_cast<float4 *>(rest), s);
+  char *rest = static_cast<char *>(ws) + quantized_bytes(rows, p->K);
   float *logits = reinterpret_cast<float *>(rest);
   const int64_t ld = score_ld(p->N);
-  st = launch_linear_i8(p, xq, ld_xq, xs, rows, nullptr, logits, AVEY_F32, ld, s);
+  if (linear_few_quantizes(x_dt, rows, p->K)) {
+    st = launch_linear_few(p, x, x_dt, ld_x, nullptr, prenorm ? 1 : 0, rows, nullptr, logits, AVEY_F32, ld, s);
+  } else {
+    const int8_t *xq = static_cast<const int8_t *>(x);
+    const float *xs = x_scale;
+    int64_t ld_xq = ld_x;
+    if (x_dt != AVEY_I8) {
+      st = quantize_to_ws(p, x, x_dt, ld_x, prenorm, rows, ws, &xq, &ld_xq, &xs, s);
+      if (st != AVEY_OK) return st;
+    }
+    if (rows > kFewRows)
+      return launch_score_i8(p, xq, ld_xq, xs, rows, ids, logprob, stats, entropy,
+                             reinterpret_cast<float4 *>(rest), s);
+    st = launch_linear_i8(p, xq, ld_xq, xs, rows, nullptr, logits, AVEY_F32, ld, s);
+  }
   if (st != AVEY_OK) return st;
   return launch_token_logprobs(logits, AVEY_F32, rows, p->N, ld, ids, 0, logprob, stats, entropy, nullptr,
                                nullptr, s);

@@ -152,7 +152,8 @@ def _product(x, q, w, b, act, res):
 
 
 SHAPES = [(1, 768, 1000), (1, 5, 1), (2, 16, 7), (7, 31, 64), (8, 768, 257), (9, 127, 65), (16, 128, 8),
-          (33, 129, 255), (64, 768, 1536), (129, 1000, 96), (257, 100, 300), (300, 2048, 33), (1025, 64, 513)]
+          (33, 129, 255), (64, 768, 1536), (129, 1000, 96), (257, 100, 300), (300, 2048, 33), (1025, 64, 513), (24, 500, 77),
+          (30, 5000, 40), (12, 7000, 9700), (17, 64, 1), (32, 1025, 130)]
 
 
 @pytest.mark.parametrize("rows,K,N", SHAPES)

@@ -41,7 +41,7 @@ def _params(**kw):
 
 
 def _linear(p=None, **kw):
-    a = dict(x=A, dt=av.AVEY_F32, ld=40, xs=None, prenorm=0, rows=4, res=None, out=A, odt=av.AVEY_F32, ldo=24,
+    a = dict(x=A, dt=av.AVEY_F32, ld=40, xs=None, prenorm=0, rows=40, res=None, out=A, odt=av.AVEY_F32, ldo=24,
              ws=A, wsb=1 << 20)
     a.update(kw)
     q = _params() if p is None else p
@@ -75,6 +75,9 @@ def test_linear_i8_refuses_null_params_and_sizes_its_workspace():
     assert L.avey_linear_i8(None, A, 0, 40, None, 0, 4, None, A, 0, 24, A, 1 << 20, None) == 1
     assert L.avey_linear_i8_workspace_bytes(av.AVEY_I8, 100, 40) == 0
     assert L.avey_linear_i8_workspace_bytes(av.AVEY_F32, 0, 40) == 0
+    # few rows are rounded by the product's own kernel
+    assert L.avey_linear_i8_workspace_bytes(av.AVEY_F32, 16, 40) == 0
+    assert L.avey_linear_i8_workspace_bytes(av.AVEY_F32, 17, 40) == (17 * 48 + 255) // 256 * 256 + 256
     assert L.avey_linear_i8_workspace_bytes(av.AVEY_F32, 100, 40) == (100 * 48 + 255) // 256 * 256 + 512
 
 
