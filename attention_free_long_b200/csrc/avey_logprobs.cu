@@ -34,6 +34,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
 // exp(d) is 0 in fp32 from here down; keeps 0 * (x - m) finite
 constexpr float kFar = -200.0f;
+// down to here x - m is finite for every m
+constexpr float kLow = -1e30f;
 constexpr uint32_t kOrdNegInf = 0x007fffffu;
 
 __device__ __forceinline__ float fast_exp(float d) {
@@ -70,6 +72,19 @@ struct Vec<float> {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                       __float_as_uint(v[3]));
   }
+  static constexpr uint32_t kNegInf = 0xff800000u;
+  static __device__ __forceinline__ float max(const uint4 &w) {
+    return fmaxf(max3f(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z)), __uint_as_float(w.w));
+  }
+  static __device__ __forceinline__ float min(const uint4 *w, int n) {
+    float m = INFINITY;
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      m = fminf(fminf(fminf(m, __uint_as_float(w[i].x)), __uint_as_float(w[i].y)),
+                fminf(__uint_as_float(w[i].z), __uint_as_float(w[i].w)));
+    return m;
+  }
+  static __device__ __forceinline__ void set(uint32_t *w, int i, float x) { w[i] = __float_as_uint(x); }
   static __device__ __forceinline__ float to_f(float x) { return x; }
   static __device__ __forceinline__ float from_f(float x) { return x; }
 };
@@ -87,6 +102,25 @@ struct Vec<bf16> {
   static __device__ __forceinline__ uint4 pack(const float *v) {
     return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                       pack_bf16(v[6], v[7]));
+  }
+  static constexpr uint32_t kNegInf = 0xff80ff80u;
+  static __device__ __forceinline__ __nv_bfloat162 b2(uint32_t w) {
+    return *reinterpret_cast<const __nv_bfloat162 *>(&w);
+  }
+  static __device__ __forceinline__ float max(const uint4 &w) {
+    const __nv_bfloat162 m = __hmax2(__hmax2(b2(w.x), b2(w.y)), __hmax2(b2(w.z), b2(w.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ float min(const uint4 *w, int n) {
+    __nv_bfloat162 m = b2(w[0].x);
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      m = __hmin2(__hmin2(__hmin2(m, b2(w[i].x)), b2(w[i].y)), __hmin2(b2(w[i].z), b2(w[i].w)));
+    return fminf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ void set(uint32_t *w, int i, bf16 x) {
+    const uint32_t b = __bfloat16_as_ushort(x);
+    w[i / 2] = (i & 1) ? (w[i / 2] & 0x0000ffffu) | (b << 16) : (w[i / 2] & 0xffff0000u) | b;
   }
   static __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ bf16 from_f(float x) { return __float2bfloat16_rn(x); }
@@ -108,22 +142,16 @@ struct Row {
     const int e = first(u);
     return e >= 0 && e <= V - N;
   }
-  __device__ __forceinline__ uint4 load_whole(int u) const {
-    return __ldg(reinterpret_cast<const uint4 *>(p + first(u)));
-  }
-  // elements that do not exist are -inf; plain loads, as the gradient may
-  // overwrite the row it reads
-  __device__ __forceinline__ void load_part(int u, float *v) const {
+  // Elements that do not exist are -inf.  Plain loads, as the gradient may
+  // overwrite the row it reads.
+  __device__ __forceinline__ uint4 load(int u) const {
     const int e = first(u);
+    if (whole(u)) return *reinterpret_cast<const uint4 *>(p + e);
+    uint32_t w[4] = {Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf};
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      v[i] = (e + i >= 0 && e + i < V) ? Vec<T>::to_f(p[e + i]) : -INFINITY;
-  }
-  __device__ __forceinline__ void load(int u, float *v) const {
-    if (whole(u))
-      Vec<T>::unpack(*reinterpret_cast<const uint4 *>(p + first(u)), v);
-    else
-      load_part(u, v);
+      if (e + i >= 0 && e + i < V) Vec<T>::set(w, i, p[e + i]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 
@@ -136,6 +164,58 @@ __device__ __forceinline__ void rebase(Stat &a, float M) {
   a.t = f * fmaf(a.s, d, a.t);
   a.s *= f;
   a.m = M;
+}
+
+// One vector's terms into two running pairs of sums.  CLAMP: some elements are
+// so low that x - m may be infinite.
+template <typename T, bool CLAMP>
+__device__ __forceinline__ void add_terms(const uint4 &w, float m, float2 &s, float2 &t) {
+  constexpr int N = Vec<T>::N;
+  float v[N];
+  Vec<T>::unpack(w, v);
+  const float2 minus = make_float2(-m, -m), l2 = make_float2(kLog2e, kLog2e);
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    float2 d = fadd2(make_float2(v[j], v[j + 1]), minus);
+    const float2 y = fmul2(d, l2);
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
+    if (CLAMP) d = make_float2(fmaxf(d.x, kFar), fmaxf(d.y, kFar));
+    s = fadd2(s, e);
+    t = ffma2(e, d, t);
+  }
+}
+
+// A batch of vectors u, u + stride, .. into a thread's statistics and, with
+// TOP, its largest value and the first vector that holds it.
+template <typename T, bool TOP>
+__device__ __forceinline__ void add_batch(const uint4 (&w)[kBatch], int u, int stride, Stat &st, float2 &s,
+                                          float2 &t, float &best, int &best_vec) {
+  float top = st.m;
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const float vm = Vec<T>::max(w[i]);
+    if (TOP && vm > best) {
+      best = vm;
+      best_vec = u + i * stride;
+    }
+    top = fmaxf(top, vm);
+  }
+  if (top > st.m) {
+    st.s = s.x + s.y;
+    st.t = t.x + t.y;
+    rebase(st, top);
+    s = make_float2(st.s, 0.f);
+    t = make_float2(st.t, 0.f);
+  }
+  if (Vec<T>::min(w, kBatch) >= kLow) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) add_terms<T, false>(w[i], st.m, s, t);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) add_terms<T, true>(w[i], st.m, s, t);
+  }
 }
 
 struct LpArgs {
@@ -196,12 +276,12 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t a) {
   return v;
 }
 
-template <typename T, bool CLUSTER>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs(const LpArgs a) {
+template <typename T, bool CLUSTER, bool TOP>
+__global__ void __launch_bounds__(kLpThreads, 4) token_logprobs(const LpArgs a) {
   constexpr int N = Vec<T>::N;
   __shared__ float s_m[kLpWarps], s_s[kLpWarps], s_t[kLpWarps];
   __shared__ float s_out[3];
-  __shared__ uint64_t lists[kLpWarps][32];
+  __shared__ uint64_t lists[TOP ? kLpWarps : 1][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = CLUSTER ? a.blocks : 1;
   const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
@@ -223,46 +303,30 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs(const LpArgs a) {
   Stat st{kLowest, 0.f, 0.f};
   float best = -INFINITY;
   int best_vec = 0;
-  for (int u0 = me; u0 < r.vecs; u0 += kBatch * stride) {
-    uint4 w[kBatch];
-    float v[kBatch][N];
+  {
+    float2 s2 = make_float2(0.f, 0.f), t2 = s2;
+    const int whole_end = static_cast<int>((static_cast<long long>(a.V) + r.shift) / N);
+    int u = me;
+    if (r.shift == 0 || u > 0) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(r.p - r.shift);  // vector 0, of which 0 .. shift - 1 is not ours
+      for (; u + (kBatch - 1) * stride < whole_end; u += kBatch * stride) {
+        uint4 w[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const long long u = u0 + static_cast<long long>(i) * stride;
-      if (u < r.vecs && r.whole(static_cast<int>(u))) w[i] = r.load_whole(static_cast<int>(u));
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const long long u = u0 + static_cast<long long>(i) * stride;
-      if (u < r.vecs && r.whole(static_cast<int>(u))) {
-        Vec<T>::unpack(w[i], v[i]);
-      } else if (u < r.vecs) {
-        r.load_part(static_cast<int>(u), v[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[i][j] = -INFINITY;
+        for (int i = 0; i < kBatch; ++i) w[i] = __ldg(src + u + i * stride);
+        add_batch<T, TOP>(w, u, stride, st, s2, t2, best, best_vec);
       }
     }
+    for (; u < r.vecs; u += kBatch * stride) {
+      uint4 w[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      float vm = v[i][0];
-#pragma unroll
-      for (int j = 1; j < N; ++j) vm = fmaxf(vm, v[i][j]);
-      if (vm > best) {
-        best = vm;
-        best_vec = u0 + i * stride;
+      for (int i = 0; i < kBatch; ++i) {
+        w[i] = make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf);
+        if (u + i * stride < r.vecs) w[i] = r.load(u + i * stride);
       }
+      add_batch<T, TOP>(w, u, stride, st, s2, t2, best, best_vec);
     }
-    if (best > st.m) rebase(st, best);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float d = v[i][j] - st.m, e = fast_exp(d);
-        st.s += e;
-        st.t = fmaf(e, fmaxf(d, kFar), st.t);
-      }
-    }
+    st.s = s2.x + s2.y;
+    st.t = t2.x + t2.y;
   }
 
   // ---- the row's (m, s, t)
@@ -278,7 +342,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs(const LpArgs a) {
     s_s[warp] = st.s;
     s_t[warp] = st.t;
   }
-  if (a.top > 0) {
+  if constexpr (TOP) {
     lists[warp][lane] = warp_sort(my_key, lane);
     block_merge(lists, warp, lane);
   } else {
@@ -322,7 +386,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs(const LpArgs a) {
       all.s += part[c].s;
       all.t += part[c].t;
     }
-    if (a.top > 0) {
+    if constexpr (TOP) {
       uint64_t key = 0;
       if (warp == 0)
         for (int c = 0; c < C; ++c) key = warp_merge(key, ld_cluster_u64(mapa_shared(laddr, c)), lane);
@@ -347,7 +411,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs(const LpArgs a) {
   }
 
   // ---- alternatives
-  if (a.top > 0) {
+  if constexpr (TOP) {
     const uint64_t last = lists[0][a.top - 1];
     const uint32_t bar = last ? static_cast<uint32_t>(last >> 32) : kOrdNegInf + 1u;
     uint64_t list = 0;  // this warp's best, descending over the lanes
@@ -361,7 +425,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs(const LpArgs a) {
         const long long u = u0 + static_cast<long long>(lane) * stride;
         float v[N];
         if (u < r.vecs) {
-          r.load(static_cast<int>(u), v);
+          Vec<T>::unpack(r.load(static_cast<int>(u)), v);
         } else {
 #pragma unroll
           for (int j = 0; j < N; ++j) v[j] = -INFINITY;
@@ -428,7 +492,10 @@ avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
   while (C < 8 && static_cast<long long>(rows) * C * 2 <= 2ll * sms && vecs >= 2ll * C * kLpThreads) C *= 2;
   a.blocks = C;
   if (C == 1) {
-    token_logprobs<T, false><<<rows, kLpThreads, 0, s>>>(a);
+    if (a.top > 0)
+      token_logprobs<T, false, true><<<rows, kLpThreads, 0, s>>>(a);
+    else
+      token_logprobs<T, false, false><<<rows, kLpThreads, 0, s>>>(a);
   } else {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * C);
@@ -441,7 +508,9 @@ avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, token_logprobs<T, true>, static_cast<const LpArgs>(a));
+    const cudaError_t e = 
+        a.top > 0 ? cudaLaunchKernelEx(&cfg, token_logprobs<T, true, true>, static_cast<const LpArgs>(a))
+                  : cudaLaunchKernelEx(&cfg, token_logprobs<T, true, false>, static_cast<const LpArgs>(a));
     if (e != cudaSuccess) {
       cudaGetLastError();
       set_detail("token_logprobs launch failed: %s", cudaGetErrorString(e));
@@ -465,7 +534,8 @@ struct LpGradArgs {
   int *status;
 };
 
-constexpr int kGradVecs = 8;  // vectors a thread takes at most
+constexpr int kGradBatch = 4;  // vectors a thread loads at once
+constexpr int kGradVecs = 8;   // and takes at most
 
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads) token_logprobs_grad(const LpGradArgs a) {
@@ -486,29 +556,55 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_grad(const LpGradAr
   const float2 st = reinterpret_cast<const float2 *>(a.stats)[row];
   const float H = a.d_entropy ? a.entropy[row] : 0.f;
   const bool none = (g == 0.f && h == 0.f) || st.x == -INFINITY;
+  const float2 m2 = make_float2(-st.x, -st.x), z2 = make_float2(-st.y, -st.y);
+  const float2 h2 = make_float2(-h, -h), c2 = make_float2(-fmaf(h, H, g), -fmaf(h, H, g));
+  const float2 l2 = make_float2(kLog2e, kLog2e);
   const int per = (r.vecs + a.parts - 1) / a.parts;
   const int end = min(r.vecs, (part + 1) * per);
-  for (int u = part * per + static_cast<int>(threadIdx.x); u < end; u += kLpThreads) {
-    const int e0 = r.first(u);
-    float v[N];
-    if (none) {
+  for (int u0 = part * per + static_cast<int>(threadIdx.x); u0 < end; u0 += kGradBatch * kLpThreads) {
+    uint4 w[kGradBatch];
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = 0.f;
-    } else {
-      r.load(u, v);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float lp = (v[j] - st.x) - st.y, p = fast_exp(lp);
-        v[j] = -p * fmaf(h, fmaxf(lp, kFar) + H, g);
-        if (e0 + j == id) v[j] += g;
-      }
+    for (int i = 0; i < kGradBatch; ++i) {
+      const int u = u0 + i * kLpThreads;
+      if (u < end && !none) w[i] = r.load(u);
     }
-    if (same && r.whole(u)) {
-      *reinterpret_cast<uint4 *>(out + e0) = Vec<T>::pack(v);
-    } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (e0 + j >= 0 && e0 + j < a.V) out[e0 + j] = Vec<T>::from_f(v[j]);
+    for (int i = 0; i < kGradBatch; ++i) {
+      const int u = u0 + i * kLpThreads;
+      if (u >= end) break;
+      const int e0 = r.first(u);
+      float v[N];
+      if (none) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = 0.f;
+      } else {
+        Vec<T>::unpack(w[i], v);
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+          // log p, kept finite (NaN too stays) so that 0 * log p is 0
+          float2 lp = fadd2(fadd2(make_float2(v[j], v[j + 1]), m2), z2);
+          lp = make_float2(max_nan(lp.x, kFar), max_nan(lp.y, kFar));
+          const float2 y = fmul2(lp, l2);
+          float2 p;
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(y.x));
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(y.y));
+          const float2 d = fmul2(p, ffma2(h2, lp, c2));
+          v[j] = d.x;
+          v[j + 1] = d.y;
+        }
+        if (static_cast<unsigned>(id - e0) < static_cast<unsigned>(N)) {
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (e0 + j == id) v[j] += g;
+        }
+      }
+      if (same && r.whole(u)) {
+        *reinterpret_cast<uint4 *>(out + e0) = Vec<T>::pack(v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (e0 + j >= 0 && e0 + j < a.V) out[e0 + j] = Vec<T>::from_f(v[j]);
+      }
     }
   }
 }
