@@ -6,17 +6,13 @@
 //
 // Forward: one pass over the row with a running maximum; each thread carries
 // (m, s, t) = (max, sum e, sum e (x - m)) and rescales s and t once a batch
-// when its maximum grows.  A row belongs to one block, or to a cluster of up
-// to eight blocks when there are few rows, whose partial results meet in
-// distributed shared memory.
-// Alternatives: beside its maximum a thread keeps the vector it came from.
-// Every true alternative lies with one of the `top` threads of largest
-// (maximum, first vector): the vectors of different threads are disjoint
-// index ranges, so each of those threads holds an element that beats
-// everything of a thread behind them.  Only these threads' vectors (top / 256
-// of the row) are read a second time, an element below the last of those
-// maxima is dropped at once, and the rest goes through sorted 32-entry lists,
-// one a warp.
+// when its maximum grows.  A row belongs to one block, or to a cluster of up to eight blocks when there are
+// few rows, whose partial results meet in distributed shared memory.
+// Alternatives: the `top`-th largest of the threads' maxima is a bar that `top`
+// elements reach, so every alternative reaches it and lies with a thread whose
+// maximum does: about `top` of them.  Their vectors (top / 256 of the row) are
+// read a second time, and what reaches the bar goes through sorted lists, one a
+// warp.  The streaming loop carries nothing for this.
 // Backward: dx_j = g (1[j = id] - p_j) - h p_j (log p_j + entropy), one read and
 // one write of the row.
 #include <algorithm>
@@ -29,7 +25,7 @@ namespace avey {
 namespace {
 
 constexpr int kLpThreads = 256, kLpWarps = 8;
-constexpr int kBatch = 4;             // 16-byte vectors a thread loads at once
+constexpr int kBatch = 4;             // 16-byte vectors a thread takes at once
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
 // exp(d) is 0 in fp32 from here down; keeps 0 * (x - m) finite
@@ -57,6 +53,12 @@ __device__ __forceinline__ uint64_t key_of(float f, uint32_t index) {
   return (static_cast<uint64_t>(ord_of(f)) << 32) | (~index);
 }
 
+__device__ __forceinline__ float min3f(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <typename T>
 struct Vec;
 template <>
@@ -76,12 +78,15 @@ struct Vec<float> {
   static __device__ __forceinline__ float max(const uint4 &w) {
     return fmaxf(max3f(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z)), __uint_as_float(w.w));
   }
-  static __device__ __forceinline__ float min(const uint4 *w, int n) {
+  static __device__ __forceinline__ float max4(const uint4 *w) {
+    return fmaxf(max3f(max(w[0]), max(w[1]), max(w[2])), max(w[3]));
+  }
+  static __device__ __forceinline__ float min4(const uint4 *w) {
     float m = INFINITY;
 #pragma unroll
-    for (int i = 0; i < n; ++i)
-      m = fminf(fminf(fminf(m, __uint_as_float(w[i].x)), __uint_as_float(w[i].y)),
-                fminf(__uint_as_float(w[i].z), __uint_as_float(w[i].w)));
+    for (int i = 0; i < 4; ++i)
+      m = min3f(min3f(m, __uint_as_float(w[i].x), __uint_as_float(w[i].y)), __uint_as_float(w[i].z),
+                __uint_as_float(w[i].w));
     return m;
   }
   static __device__ __forceinline__ void set(uint32_t *w, int i, float x) { w[i] = __float_as_uint(x); }
@@ -111,10 +116,17 @@ struct Vec<bf16> {
     const __nv_bfloat162 m = __hmax2(__hmax2(b2(w.x), b2(w.y)), __hmax2(b2(w.z), b2(w.w)));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  static __device__ __forceinline__ float min(const uint4 *w, int n) {
+  static __device__ __forceinline__ float max4(const uint4 *w) {
     __nv_bfloat162 m = b2(w[0].x);
 #pragma unroll
-    for (int i = 0; i < n; ++i)
+    for (int i = 0; i < 4; ++i)
+      m = __hmax2(__hmax2(__hmax2(m, b2(w[i].x)), b2(w[i].y)), __hmax2(b2(w[i].z), b2(w[i].w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ float min4(const uint4 *w) {
+    __nv_bfloat162 m = b2(w[0].x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
       m = __hmin2(__hmin2(__hmin2(m, b2(w[i].x)), b2(w[i].y)), __hmin2(b2(w[i].z), b2(w[i].w)));
     return fminf(__low2float(m), __high2float(m));
   }
@@ -187,21 +199,10 @@ __device__ __forceinline__ void add_terms(const uint4 &w, float m, float2 &s, fl
   }
 }
 
-// A batch of vectors u, u + stride, .. into a thread's statistics and, with
-// TOP, its largest value and the first vector that holds it.
-template <typename T, bool TOP>
-__device__ __forceinline__ void add_batch(const uint4 (&w)[kBatch], int u, int stride, Stat &st, float2 &s,
-                                          float2 &t, float &best, int &best_vec) {
-  float top = st.m;
-#pragma unroll
-  for (int i = 0; i < kBatch; ++i) {
-    const float vm = Vec<T>::max(w[i]);
-    if (TOP && vm > best) {
-      best = vm;
-      best_vec = u + i * stride;
-    }
-    top = fmaxf(top, vm);
-  }
+// A batch of vectors into a thread's statistics; s and t are the running sums.
+template <typename T>
+__device__ __forceinline__ void add_batch(const uint4 (&w)[kBatch], Stat &st, float2 &s, float2 &t) {
+  const float top = Vec<T>::max4(w);
   if (top > st.m) {
     st.s = s.x + s.y;
     st.t = t.x + t.y;
@@ -209,13 +210,64 @@ __device__ __forceinline__ void add_batch(const uint4 (&w)[kBatch], int u, int s
     s = make_float2(st.s, 0.f);
     t = make_float2(st.t, 0.f);
   }
-  if (Vec<T>::min(w, kBatch) >= kLow) {
+  if (Vec<T>::min4(w) >= kLow) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) add_terms<T, false>(w[i], st.m, s, t);
   } else {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) add_terms<T, true>(w[i], st.m, s, t);
   }
+}
+
+
+// Descending sort of one value per lane.
+__device__ __forceinline__ uint32_t warp_sort(uint32_t v, int lane) {
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1) {
+#pragma unroll
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, v, j);
+      v = ((lane & j) == 0) == ((lane & k) == 0) ? max(v, o) : min(v, o);
+    }
+  }
+  return v;
+}
+
+// The L largest of two descending lists of L lanes each, descending; o is the
+// second list reversed.
+template <int L, typename K>
+__device__ __forceinline__ K merge_reversed(K v, K o, int lane) {
+  v = max(v, o);
+#pragma unroll
+  for (int j = L / 2; j > 0; j >>= 1) {
+    o = __shfl_xor_sync(0xffffffffu, v, j);
+    v = (lane & j) == 0 ? max(v, o) : min(v, o);
+  }
+  return v;
+}
+// The L largest of eight descending lists (list i at lists + 32 i), in every
+// group of L lanes.  A warp takes L / 4 of them a lane side by side.
+template <int L, typename K>
+__device__ __forceinline__ K merge_lists(const K *lists, int lane) {
+  constexpr int R = L / 4;
+  K r[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) r[i] = lists[(i * (32 / L) + lane / L) * 32 + (lane & (L - 1))];
+#pragma unroll
+  for (int n = R / 2; n > 0; n >>= 1) {
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      r[i] = merge_reversed<L>(r[i], __shfl_xor_sync(0xffffffffu, r[i + n], L - 1), lane);
+  }
+#pragma unroll
+  for (int g = L; g < 32; g <<= 1) r[0] = merge_reversed<L>(r[0], __shfl_xor_sync(0xffffffffu, r[0], 2 * g - 1), lane);
+  return r[0];
+}
+template <typename K>
+__device__ __forceinline__ K merge_top(const K *lists, int top, int lane) {
+  if (top <= 8) return merge_lists<8>(lists, lane);
+  if (top <= 16) return merge_lists<16>(lists, lane);
+  return merge_lists<32>(lists, lane);
 }
 
 struct LpArgs {
@@ -230,44 +282,134 @@ struct LpArgs {
   int *status;
 };
 
-// Descending sort of one key per lane.
-__device__ __forceinline__ uint64_t warp_sort(uint64_t key, int lane) {
+// Statistics of the block's share of a row, given to all threads.
+__device__ __forceinline__ Stat block_stats(Stat st, float (*sm)[kLpWarps], int warp, int lane) {
+  rebase(st, warp_max(st.m));
 #pragma unroll
-  for (int k = 2; k <= 32; k <<= 1) {
-#pragma unroll
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      const uint64_t o = __shfl_xor_sync(0xffffffffu, key, j);
-      const bool first = ((lane & j) == 0) == ((lane & k) == 0);
-      key = (first == (key > o)) ? key : o;
-    }
+  for (int off = 16; off > 0; off >>= 1) {
+    st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
+    st.t += __shfl_xor_sync(0xffffffffu, st.t, off);
   }
-  return key;
-}
-// The 32 largest of two descending lists, descending.
-__device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b, int lane) {
-  const uint64_t r = __shfl_sync(0xffffffffu, b, 31 - lane);
-  uint64_t key = a > r ? a : r;
-#pragma unroll
-  for (int j = 16; j > 0; j >>= 1) {
-    const uint64_t o = __shfl_xor_sync(0xffffffffu, key, j);
-    const bool first = (lane & j) == 0;
-    key = (first == (key > o)) ? key : o;
-  }
-  return key;
-}
-// The block's warps' descending lists into lists[0]; every thread calls it.
-__device__ __forceinline__ void block_merge(uint64_t (*lists)[32], int warp, int lane) {
-#pragma unroll
-  for (int h = kLpWarps / 2; h > 0; h >>= 1) {
-    __syncthreads();
-    if (warp < h) lists[warp][lane] = warp_merge(lists[warp][lane], lists[warp + h][lane], lane);
+  if (lane == 0) {
+    sm[0][warp] = st.m;
+    sm[1][warp] = st.s;
+    sm[2][warp] = st.t;
   }
   __syncthreads();
+  float M = sm[0][0];
+#pragma unroll
+  for (int i = 1; i < kLpWarps; ++i) M = fmaxf(M, sm[0][i]);
+  Stat all{M, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kLpWarps; ++i) {
+    Stat o{sm[0][i], sm[1][i], sm[2][i]};
+    rebase(o, M);
+    all.s += o.s;
+    all.t += o.t;
+  }
+  return all;
+}
+
+// What the statistics of a whole row say.
+struct RowResult {
+  float m, z, entropy;
+  bool empty, bad;
+  __device__ __forceinline__ explicit RowResult(const Stat &all) {
+    const float nan = __uint_as_float(0x7fc00000u);
+    empty = all.s == 0.f;
+    // a finite row has 1 <= s <= V; +inf or NaN leave an infinite maximum or a NaN sum
+    bad = !(all.s < INFINITY) || all.m == INFINITY;
+    m = bad ? nan : empty ? -INFINITY : all.m;
+    z = bad ? nan : empty ? 0.f : logf(all.s);
+    entropy = bad ? nan : empty ? 0.f : z - all.t / all.s;
+  }
+  // log probability of a word with logit x
+  __device__ __forceinline__ float logprob(float x) const { return empty ? -INFINITY : (x - m) - z; }
+};
+
+__device__ __forceinline__ void write_row(const LpArgs &a, long long row, const RowResult &res, int id, float x_id) {
+  if (a.logprob) a.logprob[row] = id < 0 ? 0.f : res.logprob(x_id);
+  if (a.stats) reinterpret_cast<float2 *>(a.stats)[row] = make_float2(res.m, res.z);
+  if (a.entropy) a.entropy[row] = res.entropy;
+}
+__device__ __forceinline__ void write_top(const LpArgs &a, long long row, const RowResult &res, uint64_t key, int lane) {
+  const bool has = !res.bad && key != 0;
+  a.top_ids[row * a.top + lane] = has ? static_cast<int32_t>(~static_cast<uint32_t>(key)) : -1;
+  a.top_lp[row * a.top + lane] =
+      res.bad ? res.m : has ? res.logprob(ord_value(static_cast<uint32_t>(key >> 32))) : -INFINITY;
+}
+
+// The given token of a row and its logit.
+template <typename T>
+__device__ __forceinline__ int given_token(const LpArgs &a, long long row, const Row<T> &r, float &x_id) {
+  int id = a.ids ? a.ids[row] : -1;
+  if (id >= a.V) {
+    record_status(a.status, AVEY_ERR_DEVICE_BOUNDS);
+    id = -1;
+  }
+  x_id = id >= 0 ? Vec<T>::to_f(r.p[id]) : 0.f;
+  return id;
+}
+
+// The elements of at least `bar` of this warp's threads (those whose maximum
+// `best` reaches it), as one descending list of 32 over the lanes.  first: the
+// first vector of lane 0.
+template <typename T>
+__device__ __forceinline__ uint64_t select_top(const Row<T> &r, int first, int stride, float best, float bar, int lane) {
+  constexpr int N = Vec<T>::N;
+  uint64_t list = 0;
+  uint32_t owners = __ballot_sync(0xffffffffu, best >= bar && best > -INFINITY);
+  while (owners) {
+    const int owner = first + __ffs(owners) - 1;
+    owners &= owners - 1;
+    for (long long u0 = owner; u0 < r.vecs; u0 += 32ll * stride) {
+      const long long u = u0 + static_cast<long long>(lane) * stride;
+      float v[N];
+      uint32_t want = 0;
+      if (u < r.vecs) {
+        Vec<T>::unpack(r.load(static_cast<int>(u)), v);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (v[j] >= bar && v[j] > -INFINITY) want |= 1u << j;
+      }
+      if (__ballot_sync(0xffffffffu, want != 0) == 0) continue;
+      // of equal values only those that would still enter the list
+      const uint64_t full = __shfl_sync(0xffffffffu, list, 31);
+      const uint32_t e0 = static_cast<uint32_t>(r.first(static_cast<int>(u)));
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if ((want >> j & 1) && key_of(v[j], e0 + j) <= full) want &= ~(1u << j);
+      uint32_t lanes = __ballot_sync(0xffffffffu, want != 0);
+      while (lanes) {
+        const int src = __ffs(lanes) - 1;
+        uint64_t mine = 0;
+        if (lane == src) {
+          const int j = __ffs(want) - 1;
+          float f = v[0];
+#pragma unroll
+          for (int q = 1; q < N; ++q) f = q == j ? v[q] : f;
+          mine = key_of(f, e0 + j);
+          want &= want - 1;
+        }
+        const uint64_t nk = __shfl_sync(0xffffffffu, mine, src);
+        const int pos = __popc(__ballot_sync(0xffffffffu, list > nk));
+        const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
+        if (lane >= pos) list = lane == pos ? nk : up;
+        lanes = __ballot_sync(0xffffffffu, want != 0);
+      }
+    }
+  }
+  return list;
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t a) {
@@ -276,44 +418,38 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t a) {
   return v;
 }
 
-template <typename T, bool CLUSTER, bool TOP>
+// A row to a block, or to a cluster of a.blocks blocks.  Block `rank` takes the
+// vectors u with u / 256 % blocks == rank.
+template <typename T, bool TOP, bool CLUSTER>
 __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs(const LpArgs a) {
   constexpr int N = Vec<T>::N;
-  __shared__ float s_m[kLpWarps], s_s[kLpWarps], s_t[kLpWarps];
+  __shared__ float sm[3][kLpWarps];
   __shared__ float s_out[3];
   __shared__ uint64_t lists[TOP ? kLpWarps : 1][32];
+  __shared__ uint32_t maxima[TOP ? kLpWarps : 1][32];
+  __shared__ uint32_t s_best[TOP ? 32 : 1];
+  __shared__ uint64_t s_top[TOP && CLUSTER ? 32 : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int C = CLUSTER ? a.blocks : 1;
-  const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
+  const int C = CLUSTER ? a.blocks : 1, rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
   const long long row = blockIdx.x / C;
-  const int stride = C * kLpThreads, me = rank * kLpThreads + static_cast<int>(threadIdx.x);
+  const int stride = C * kLpThreads;
   const Row<T> r(static_cast<const T *>(a.x) + row * a.ld, a.V);
-
-  int id = -1;
+  const bool writer = rank == 0 && threadIdx.x == 0;
   float x_id = 0.f;
-  if (a.ids != nullptr && rank == 0 && threadIdx.x == 0) {
-    id = a.ids[row];
-    if (id >= a.V) {
-      record_status(a.status, AVEY_ERR_DEVICE_BOUNDS);
-      id = -1;
-    }
-    if (id >= 0) x_id = Vec<T>::to_f(r.p[id]);
-  }
+  const int id = writer ? given_token(a, row, r, x_id) : -1;
 
   Stat st{kLowest, 0.f, 0.f};
-  float best = -INFINITY;
-  int best_vec = 0;
   {
     float2 s2 = make_float2(0.f, 0.f), t2 = s2;
     const int whole_end = static_cast<int>((static_cast<long long>(a.V) + r.shift) / N);
-    int u = me;
+    int u = rank * kLpThreads + static_cast<int>(threadIdx.x);
     if (r.shift == 0 || u > 0) {
       const uint4 *src = reinterpret_cast<const uint4 *>(r.p - r.shift);  // vector 0, of which 0 .. shift - 1 is not ours
       for (; u + (kBatch - 1) * stride < whole_end; u += kBatch * stride) {
         uint4 w[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) w[i] = __ldg(src + u + i * stride);
-        add_batch<T, TOP>(w, u, stride, st, s2, t2, best, best_vec);
+        add_batch<T>(w, st, s2, t2);
       }
     }
     for (; u < r.vecs; u += kBatch * stride) {
@@ -323,41 +459,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs(const LpArgs a) 
         w[i] = make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf);
         if (u + i * stride < r.vecs) w[i] = r.load(u + i * stride);
       }
-      add_batch<T, TOP>(w, u, stride, st, s2, t2, best, best_vec);
+      add_batch<T>(w, st, s2, t2);
     }
     st.s = s2.x + s2.y;
     st.t = t2.x + t2.y;
   }
-
-  // ---- the row's (m, s, t)
-  const uint64_t my_key = best > -INFINITY ? key_of(best, static_cast<uint32_t>(best_vec)) : 0ull;
-  rebase(st, warp_max(st.m));
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
-    st.t += __shfl_xor_sync(0xffffffffu, st.t, off);
-  }
-  if (lane == 0) {
-    s_m[warp] = st.m;
-    s_s[warp] = st.s;
-    s_t[warp] = st.t;
-  }
+  const float best = st.s > 0.f ? st.m : -INFINITY;  // this thread's maximum
+  if constexpr (TOP) maxima[warp][lane] = warp_sort(ord_of(best), lane);
+  Stat all = block_stats(st, sm, warp, lane);
+  float bar = -INFINITY;
   if constexpr (TOP) {
-    lists[warp][lane] = warp_sort(my_key, lane);
-    block_merge(lists, warp, lane);
-  } else {
-    __syncthreads();
-  }
-  float M = s_m[0];
-#pragma unroll
-  for (int i = 1; i < kLpWarps; ++i) M = fmaxf(M, s_m[i]);
-  Stat all{M, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < kLpWarps; ++i) {
-    Stat o{s_m[i], s_s[i], s_t[i]};
-    rebase(o, M);
-    all.s += o.s;
-    all.t += o.t;
+    if (warp == 0) s_best[lane] = merge_top(&maxima[0][0], a.top, lane);
   }
   if constexpr (CLUSTER) {
     if (threadIdx.x == 0) {
@@ -367,7 +479,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs(const LpArgs a) 
     }
     __syncwarp();
     cluster_sync_all();
-    const uint32_t addr = smem_u32(s_out), laddr = smem_u32(&lists[0][lane]);
+    const uint32_t addr = smem_u32(s_out);
     Stat part[8];
     float CM = kLowest;
 #pragma unroll
@@ -387,95 +499,37 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs(const LpArgs a) 
       all.t += part[c].t;
     }
     if constexpr (TOP) {
-      uint64_t key = 0;
-      if (warp == 0)
-        for (int c = 0; c < C; ++c) key = warp_merge(key, ld_cluster_u64(mapa_shared(laddr, c)), lane);
-      __syncwarp();
-      cluster_sync_all();  // every block has read the lists
-      if (warp == 0) lists[0][lane] = key;
+      // the lists of all blocks, in the place of the warps' lists
+      if (warp < C) maxima[warp][lane] = ld_cluster_u32(mapa_shared(smem_u32(&s_best[lane]), warp));
+      if (warp >= C) maxima[warp][lane] = 0;
       __syncthreads();
+      bar = ord_value(__shfl_sync(0xffffffffu, merge_top(&maxima[0][0], a.top, lane), a.top - 1));
     }
+  } else if constexpr (TOP) {
+    __syncthreads();
+    bar = ord_value(s_best[a.top - 1]);
   }
-  const bool empty = all.s == 0.f;
-  // a finite row has 1 <= s <= V; +inf or NaN leave an infinite maximum or a NaN sum
-  const bool bad = !(all.s < INFINITY) || all.m == INFINITY;
-  const float nan = __uint_as_float(0x7fc00000u);
-  const float z = logf(all.s);
-  if (rank == 0 && threadIdx.x == 0) {
-    if (a.logprob)
-      a.logprob[row] = id < 0 ? 0.f : bad ? nan : empty ? -INFINITY : (x_id - all.m) - z;
-    if (a.stats)
-      reinterpret_cast<float2 *>(a.stats)[row] =
-          bad ? make_float2(nan, nan) : empty ? make_float2(-INFINITY, 0.f) : make_float2(all.m, z);
-    if (a.entropy) a.entropy[row] = bad ? nan : empty ? 0.f : z - all.t / all.s;
-  }
-
-  // ---- alternatives
+  const RowResult res(all);
+  if (writer) write_row(a, row, res, id, x_id);
   if constexpr (TOP) {
-    const uint64_t last = lists[0][a.top - 1];
-    const uint32_t bar = last ? static_cast<uint32_t>(last >> 32) : kOrdNegInf + 1u;
-    uint64_t list = 0;  // this warp's best, descending over the lanes
-    int turn = 0;
-    for (int i = 0; i < a.top; ++i) {
-      const uint64_t k = lists[0][i];
-      if (k == 0) break;
-      const int owner = static_cast<int>(~static_cast<uint32_t>(k) % static_cast<uint32_t>(stride));
-      if (owner / kLpThreads != rank || (turn++ & (kLpWarps - 1)) != warp) continue;
-      for (long long u0 = owner; u0 < r.vecs; u0 += 32ll * stride) {
-        const long long u = u0 + static_cast<long long>(lane) * stride;
-        float v[N];
-        if (u < r.vecs) {
-          Vec<T>::unpack(r.load(static_cast<int>(u)), v);
-        } else {
-#pragma unroll
-          for (int j = 0; j < N; ++j) v[j] = -INFINITY;
-        }
-        const uint64_t full = __shfl_sync(0xffffffffu, list, 31);
-        uint32_t want = 0;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          if (v[j] > -INFINITY && ord_of(v[j]) >= bar &&
-              key_of(v[j], static_cast<uint32_t>(r.first(static_cast<int>(u)) + j)) > full)
-            want |= 1u << j;
-        }
-        uint32_t lanes = __ballot_sync(0xffffffffu, want != 0);
-        while (lanes) {
-          const int src = __ffs(lanes) - 1;
-          uint64_t mine = 0;
-          if (lane == src) {
-            const int j = __ffs(want) - 1;
-            float f = v[0];
-#pragma unroll
-            for (int q = 1; q < N; ++q) f = q == j ? v[q] : f;
-            mine = key_of(f, static_cast<uint32_t>(r.first(static_cast<int>(u)) + j));
-            want &= want - 1;
-          }
-          const uint64_t nk = __shfl_sync(0xffffffffu, mine, src);
-          const int pos = __popc(__ballot_sync(0xffffffffu, list > nk));
-          const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
-          if (lane >= pos) list = lane == pos ? nk : up;
-          lanes = __ballot_sync(0xffffffffu, want != 0);
-        }
-      }
-    }
-    __syncthreads();  // every warp is past lists[0]
-    lists[warp][lane] = list;
-    block_merge(lists, warp, lane);
-    uint64_t key = lists[0][lane];
+    lists[warp][lane] = select_top(r, rank * kLpThreads + warp * 32, stride, best, bar, lane);
+    __syncthreads();
+    uint64_t key = 0;
+    if (warp == 0) key = merge_top(&lists[0][0], a.top, lane);
     if constexpr (CLUSTER) {
+      if (warp == 0) s_top[lane] = key;
       __syncwarp();
       cluster_sync_all();
-      if (rank == 0 && warp == 0) {
-        const uint32_t laddr = smem_u32(&lists[0][lane]);
-        for (int c = 1; c < C; ++c) key = warp_merge(key, ld_cluster_u64(mapa_shared(laddr, c)), lane);
+      if (rank == 0) {
+        if (warp < C)
+          lists[warp][lane] = ld_cluster_u64(mapa_shared(smem_u32(&s_top[lane]), warp));
+        else
+          lists[warp][lane] = 0;
+        __syncthreads();
+        if (warp == 0) key = merge_top(&lists[0][0], a.top, lane);
       }
     }
-    if (rank == 0 && warp == 0 && lane < a.top) {
-      const bool has = !bad && key != 0;
-      a.top_ids[row * a.top + lane] = has ? static_cast<int32_t>(~static_cast<uint32_t>(key)) : -1;
-      a.top_lp[row * a.top + lane] =
-          bad ? nan : has ? (ord_value(static_cast<uint32_t>(key >> 32)) - all.m) - z : -INFINITY;
-    }
+    if (rank == 0 && warp == 0 && lane < a.top) write_top(a, row, res, key, lane);
   }
   if constexpr (CLUSTER) {
     __syncwarp();
@@ -483,7 +537,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs(const LpArgs a) 
   }
 }
 
-template <typename T>
+template <typename T, bool TOP>
 avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
   // few rows: several blocks a row, as long as each thread still has a vector
   const int sms = sm_count();
@@ -492,10 +546,7 @@ avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
   while (C < 8 && static_cast<long long>(rows) * C * 2 <= 2ll * sms && vecs >= 2ll * C * kLpThreads) C *= 2;
   a.blocks = C;
   if (C == 1) {
-    if (a.top > 0)
-      token_logprobs<T, false, true><<<rows, kLpThreads, 0, s>>>(a);
-    else
-      token_logprobs<T, false, false><<<rows, kLpThreads, 0, s>>>(a);
+    token_logprobs<T, TOP, false><<<rows, kLpThreads, 0, s>>>(a);
   } else {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * C);
@@ -508,9 +559,7 @@ avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t e = 
-        a.top > 0 ? cudaLaunchKernelEx(&cfg, token_logprobs<T, true, true>, static_cast<const LpArgs>(a))
-                  : cudaLaunchKernelEx(&cfg, token_logprobs<T, true, false>, static_cast<const LpArgs>(a));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, true>, static_cast<const LpArgs>(a));
     if (e != cudaSuccess) {
       cudaGetLastError();
       set_detail("token_logprobs launch failed: %s", cudaGetErrorString(e));
@@ -559,52 +608,63 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_grad(const LpGradAr
   const float2 m2 = make_float2(-st.x, -st.x), z2 = make_float2(-st.y, -st.y);
   const float2 h2 = make_float2(-h, -h), c2 = make_float2(-fmaf(h, H, g), -fmaf(h, H, g));
   const float2 l2 = make_float2(kLog2e, kLog2e);
-  const int per = (r.vecs + a.parts - 1) / a.parts;
-  const int end = min(r.vecs, (part + 1) * per);
-  for (int u0 = part * per + static_cast<int>(threadIdx.x); u0 < end; u0 += kGradBatch * kLpThreads) {
-    uint4 w[kGradBatch];
+  // The gradient of the words of one vector; element `hot` of it is the given one.
+  auto gradient = [&](const uint4 &w, float (&v)[N], int hot) {
+    Vec<T>::unpack(w, v);
 #pragma unroll
-    for (int i = 0; i < kGradBatch; ++i) {
-      const int u = u0 + i * kLpThreads;
-      if (u < end && !none) w[i] = r.load(u);
+    for (int j = 0; j < N; j += 2) {
+      // log p, kept finite (NaN too stays) so that 0 * log p is 0
+      float2 lp = fadd2(fadd2(make_float2(v[j], v[j + 1]), m2), z2);
+      lp = make_float2(max_nan(lp.x, kFar), max_nan(lp.y, kFar));
+      const float2 y = fmul2(lp, l2);
+      float2 p;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(y.x));
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(y.y));
+      const float2 d = fmul2(p, ffma2(h2, lp, c2));
+      v[j] = d.x;
+      v[j + 1] = d.y;
     }
+    if (static_cast<unsigned>(hot) < static_cast<unsigned>(N)) {
 #pragma unroll
-    for (int i = 0; i < kGradBatch; ++i) {
-      const int u = u0 + i * kLpThreads;
-      if (u >= end) break;
-      const int e0 = r.first(u);
-      float v[N];
-      if (none) {
+      for (int j = 0; j < N; ++j)
+        if (j == hot) v[j] += g;
+    }
+  };
+  const int per = (r.vecs + a.parts - 1) / a.parts;
+  const int begin = part * per, end = min(r.vecs, begin + per);
+  const int hi = static_cast<int>((static_cast<long long>(a.V) + r.shift) / N);
+  int u = begin + static_cast<int>(threadIdx.x);
+  const int fast_end = same && !none ? min(end, hi) : 0;
+  if (u > 0 || r.shift == 0) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(r.p - r.shift);
+    uint4 *dst = reinterpret_cast<uint4 *>(out - r.shift);
+    for (; u + (kGradBatch - 1) * kLpThreads < fast_end; u += kGradBatch * kLpThreads) {
+      uint4 w[kGradBatch];
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = 0.f;
-      } else {
-        Vec<T>::unpack(w[i], v);
+      for (int i = 0; i < kGradBatch; ++i) w[i] = src[u + i * kLpThreads];
 #pragma unroll
-        for (int j = 0; j < N; j += 2) {
-          // log p, kept finite (NaN too stays) so that 0 * log p is 0
-          float2 lp = fadd2(fadd2(make_float2(v[j], v[j + 1]), m2), z2);
-          lp = make_float2(max_nan(lp.x, kFar), max_nan(lp.y, kFar));
-          const float2 y = fmul2(lp, l2);
-          float2 p;
-          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(y.x));
-          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(y.y));
-          const float2 d = fmul2(p, ffma2(h2, lp, c2));
-          v[j] = d.x;
-          v[j + 1] = d.y;
-        }
-        if (static_cast<unsigned>(id - e0) < static_cast<unsigned>(N)) {
-#pragma unroll
-          for (int j = 0; j < N; ++j)
-            if (e0 + j == id) v[j] += g;
-        }
+      for (int i = 0; i < kGradBatch; ++i) {
+        float v[N];
+        gradient(w[i], v, id - r.first(u + i * kLpThreads));
+        dst[u + i * kLpThreads] = Vec<T>::pack(v);
       }
-      if (same && r.whole(u)) {
-        *reinterpret_cast<uint4 *>(out + e0) = Vec<T>::pack(v);
-      } else {
+    }
+  }
+  for (; u < end; u += kLpThreads) {
+    const int e0 = r.first(u);
+    float v[N];
+    if (none) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (e0 + j >= 0 && e0 + j < a.V) out[e0 + j] = Vec<T>::from_f(v[j]);
-      }
+      for (int j = 0; j < N; ++j) v[j] = 0.f;
+    } else {
+      gradient(r.load(u), v, id >= 0 ? id - e0 : -1);
+    }
+    if (same && r.whole(u)) {
+      *reinterpret_cast<uint4 *>(out + e0) = Vec<T>::pack(v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (e0 + j >= 0 && e0 + j < a.V) out[e0 + j] = Vec<T>::from_f(v[j]);
     }
   }
 }
@@ -655,7 +715,8 @@ avey_status launch_token_logprobs(const void *logits, avey_dtype dt, int rows, i
   a.top_ids = top_ids;
   a.top_lp = top_lp;
   a.status = device_status_word();
-  return dt == AVEY_F32 ? run_logprobs<float>(a, rows, s) : run_logprobs<bf16>(a, rows, s);
+  if (dt == AVEY_F32) return top > 0 ? run_logprobs<float, true>(a, rows, s) : run_logprobs<float, false>(a, rows, s);
+  return top > 0 ? run_logprobs<bf16, true>(a, rows, s) : run_logprobs<bf16, false>(a, rows, s);
 }
 
 }  // namespace avey
