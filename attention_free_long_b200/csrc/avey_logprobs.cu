@@ -24,7 +24,7 @@
 namespace avey {
 namespace {
 
-constexpr int kLpThreads = 256, kLpWarps = 8;
+constexpr int kLpThreads = 256;       // threads of the gradient's blocks
 constexpr int kBatch = 4;             // 16-byte vectors a thread takes at once
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
@@ -32,7 +32,6 @@ constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar = -200.0f;
 // down to here x - m is finite for every m
 constexpr float kLow = -1e30f;
-constexpr uint32_t kOrdNegInf = 0x007fffffu;
 
 __device__ __forceinline__ float fast_exp(float d) {
   float r;
@@ -245,11 +244,11 @@ __device__ __forceinline__ K merge_reversed(K v, K o, int lane) {
   }
   return v;
 }
-// The L largest of eight descending lists (list i at lists + 32 i), in every
-// group of L lanes.  A warp takes L / 4 of them a lane side by side.
-template <int L, typename K>
+// The L largest of W descending lists (list i at lists + 32 i), in every group
+// of L lanes.  A warp takes them side by side, 32 / L lists to a register.
+template <int L, int W, typename K>
 __device__ __forceinline__ K merge_lists(const K *lists, int lane) {
-  constexpr int R = L / 4;
+  constexpr int R = L * W / 32;
   K r[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) r[i] = lists[(i * (32 / L) + lane / L) * 32 + (lane & (L - 1))];
@@ -263,17 +262,17 @@ __device__ __forceinline__ K merge_lists(const K *lists, int lane) {
   for (int g = L; g < 32; g <<= 1) r[0] = merge_reversed<L>(r[0], __shfl_xor_sync(0xffffffffu, r[0], 2 * g - 1), lane);
   return r[0];
 }
-template <typename K>
+template <int W, typename K>
 __device__ __forceinline__ K merge_top(const K *lists, int top, int lane) {
-  if (top <= 8) return merge_lists<8>(lists, lane);
-  if (top <= 16) return merge_lists<16>(lists, lane);
-  return merge_lists<32>(lists, lane);
+  if (top <= 8) return merge_lists<8, W>(lists, lane);
+  if (top <= 16) return merge_lists<16, W>(lists, lane);
+  return merge_lists<32, W>(lists, lane);
 }
 
 struct LpArgs {
   const void *x;
   long long ld;
-  int V, blocks;  // blocks of a row (the cluster size)
+  int rows, V, blocks;  // blocks of a row (the cluster size)
   const int32_t *ids;
   int top;
   float *logprob, *stats, *entropy;
@@ -282,14 +281,16 @@ struct LpArgs {
   int *status;
 };
 
-// Statistics of the block's share of a row, given to all threads.
-__device__ __forceinline__ Stat block_stats(Stat st, float (*sm)[kLpWarps], int warp, int lane) {
+// Statistics of the share of a row that W warps hold, given to all threads.
+template <int W>
+__device__ __forceinline__ Stat row_stats(Stat st, float (*sm)[W], int warp, int lane) {
   rebase(st, warp_max(st.m));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
     st.t += __shfl_xor_sync(0xffffffffu, st.t, off);
   }
+  if constexpr (W == 1) return st;
   if (lane == 0) {
     sm[0][warp] = st.m;
     sm[1][warp] = st.s;
@@ -298,10 +299,10 @@ __device__ __forceinline__ Stat block_stats(Stat st, float (*sm)[kLpWarps], int 
   __syncthreads();
   float M = sm[0][0];
 #pragma unroll
-  for (int i = 1; i < kLpWarps; ++i) M = fmaxf(M, sm[0][i]);
+  for (int i = 1; i < W; ++i) M = fmaxf(M, sm[0][i]);
   Stat all{M, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < kLpWarps; ++i) {
+  for (int i = 0; i < W; ++i) {
     Stat o{sm[0][i], sm[1][i], sm[2][i]};
     rebase(o, M);
     all.s += o.s;
@@ -339,63 +340,82 @@ __device__ __forceinline__ void write_top(const LpArgs &a, long long row, const 
       res.bad ? res.m : has ? res.logprob(ord_value(static_cast<uint32_t>(key >> 32))) : -INFINITY;
 }
 
-// The given token of a row and its logit.
+// The logit of a row's given token; an id past the vocabulary becomes none.
 template <typename T>
-__device__ __forceinline__ int given_token(const LpArgs &a, long long row, const Row<T> &r, float &x_id) {
-  int id = a.ids ? a.ids[row] : -1;
+__device__ __forceinline__ float given_logit(const LpArgs &a, const Row<T> &r, int &id) {
   if (id >= a.V) {
     record_status(a.status, AVEY_ERR_DEVICE_BOUNDS);
     id = -1;
   }
-  x_id = id >= 0 ? Vec<T>::to_f(r.p[id]) : 0.f;
-  return id;
+  return id >= 0 ? Vec<T>::to_f(r.p[id]) : 0.f;
+}
+
+// A vector's elements of at least `bar`, one vector per lane from element e0,
+// into the warp's descending list of 32 keys over the lanes.
+template <typename T>
+__device__ __forceinline__ void insert_top(const uint4 &w, bool in, uint32_t e0, float bar, uint64_t &list, int lane) {
+  constexpr int N = Vec<T>::N;
+  uint32_t lanes = __ballot_sync(0xffffffffu, in && Vec<T>::max(w) >= bar);
+  if (lanes == 0) return;
+  float v[N];
+  uint32_t want = 0;
+  Vec<T>::unpack(w, v);
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    if (in && v[j] >= bar && v[j] > -INFINITY) want |= 1u << j;
+  if (__popc(lanes) > 4) {
+    // many equal values: only those that would still enter the list
+    const uint64_t full = __shfl_sync(0xffffffffu, list, 31);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if ((want >> j & 1) && key_of(v[j], e0 + j) <= full) want &= ~(1u << j);
+  }
+  lanes = __ballot_sync(0xffffffffu, want != 0);
+  while (lanes) {
+    const int src = __ffs(lanes) - 1;
+    uint64_t mine = 0;
+    if (lane == src) {
+      const int j = __ffs(want) - 1;
+      float f = v[0];
+#pragma unroll
+      for (int q = 1; q < N; ++q) f = q == j ? v[q] : f;
+      mine = key_of(f, e0 + j);
+      want &= want - 1;
+    }
+    const uint64_t nk = __shfl_sync(0xffffffffu, mine, src);
+    const int pos = __popc(__ballot_sync(0xffffffffu, list > nk));
+    const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
+    if (lane >= pos) list = lane == pos ? nk : up;
+    lanes = __ballot_sync(0xffffffffu, want != 0);
+  }
 }
 
 // The elements of at least `bar` of this warp's threads (those whose maximum
 // `best` reaches it), as one descending list of 32 over the lanes.  first: the
-// first vector of lane 0.
+// first vector of lane 0.  Four threads' vectors are on their way at once.
 template <typename T>
 __device__ __forceinline__ uint64_t select_top(const Row<T> &r, int first, int stride, float best, float bar, int lane) {
-  constexpr int N = Vec<T>::N;
   uint64_t list = 0;
   uint32_t owners = __ballot_sync(0xffffffffu, best >= bar && best > -INFINITY);
   while (owners) {
-    const int owner = first + __ffs(owners) - 1;
-    owners &= owners - 1;
-    for (long long u0 = owner; u0 < r.vecs; u0 += 32ll * stride) {
-      const long long u = u0 + static_cast<long long>(lane) * stride;
-      float v[N];
-      uint32_t want = 0;
-      if (u < r.vecs) {
-        Vec<T>::unpack(r.load(static_cast<int>(u)), v);
+    int owner[4];
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (v[j] >= bar && v[j] > -INFINITY) want |= 1u << j;
-      }
-      if (__ballot_sync(0xffffffffu, want != 0) == 0) continue;
-      // of equal values only those that would still enter the list
-      const uint64_t full = __shfl_sync(0xffffffffu, list, 31);
-      const uint32_t e0 = static_cast<uint32_t>(r.first(static_cast<int>(u)));
+    for (int i = 0; i < 4; ++i) {
+      owner[i] = owners ? __ffs(owners) - 1 : 32;
+      owners &= owners - 1;
+    }
+    // offset of this lane's vector of the first thread; the others' are beside it
+    for (long long u0 = first + static_cast<long long>(lane) * stride; __any_sync(0xffffffffu, u0 < r.vecs);
+         u0 += 32ll * stride) {
+      uint4 w[4];
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if ((want >> j & 1) && key_of(v[j], e0 + j) <= full) want &= ~(1u << j);
-      uint32_t lanes = __ballot_sync(0xffffffffu, want != 0);
-      while (lanes) {
-        const int src = __ffs(lanes) - 1;
-        uint64_t mine = 0;
-        if (lane == src) {
-          const int j = __ffs(want) - 1;
-          float f = v[0];
+      for (int i = 0; i < 4; ++i)
+        if (owner[i] < 32 && u0 + owner[i] < r.vecs) w[i] = r.load(static_cast<int>(u0) + owner[i]);
 #pragma unroll
-          for (int q = 1; q < N; ++q) f = q == j ? v[q] : f;
-          mine = key_of(f, e0 + j);
-          want &= want - 1;
-        }
-        const uint64_t nk = __shfl_sync(0xffffffffu, mine, src);
-        const int pos = __popc(__ballot_sync(0xffffffffu, list > nk));
-        const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
-        if (lane >= pos) list = lane == pos ? nk : up;
-        lanes = __ballot_sync(0xffffffffu, want != 0);
+      for (int i = 0; i < 4; ++i) {
+        if (owner[i] == 32) break;
+        insert_top<T>(w[i], u0 + owner[i] < r.vecs, static_cast<uint32_t>(r.first(static_cast<int>(u0) + owner[i])),
+                      bar, list, lane);
       }
     }
   }
@@ -418,31 +438,33 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t a) {
   return v;
 }
 
-// A row to a block, or to a cluster of a.blocks blocks.  Block `rank` takes the
-// vectors u with u / 256 % blocks == rank.
-template <typename T, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(kLpThreads, 4) token_logprobs(const LpArgs a) {
+// W warps to a row: one (four rows a block), or all of a block's; or, with
+// CLUSTER, a cluster of a.blocks blocks, block `rank` taking the vectors u with
+// u / (32 W) % blocks == rank.
+template <typename T, bool TOP, int W, bool CLUSTER>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? 8 : 32 / W) token_logprobs(const LpArgs a) {
   constexpr int N = Vec<T>::N;
-  __shared__ float sm[3][kLpWarps];
+  static_assert(!CLUSTER || W == 8, "clusters are made of blocks of eight warps");
+  __shared__ float sm[3][W];
   __shared__ float s_out[3];
-  __shared__ uint64_t lists[TOP ? kLpWarps : 1][32];
-  __shared__ uint32_t maxima[TOP ? kLpWarps : 1][32];
+  __shared__ uint64_t lists[TOP && W > 1 ? W : 1][32];
+  __shared__ uint32_t maxima[TOP && W > 1 ? W : 1][32];
   __shared__ uint32_t s_best[TOP ? 32 : 1];
   __shared__ uint64_t s_top[TOP && CLUSTER ? 32 : 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = W == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = CLUSTER ? a.blocks : 1, rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
-  const long long row = blockIdx.x / C;
-  const int stride = C * kLpThreads;
+  const long long row = W == 1 ? blockIdx.x * 4ll + (threadIdx.x >> 5) : blockIdx.x / C;
+  if (W == 1 && row >= a.rows) return;
+  const int stride = C * 32 * W;
   const Row<T> r(static_cast<const T *>(a.x) + row * a.ld, a.V);
-  const bool writer = rank == 0 && threadIdx.x == 0;
-  float x_id = 0.f;
-  const int id = writer ? given_token(a, row, r, x_id) : -1;
+  const bool writer = rank == 0 && warp == 0 && lane == 0;
+  int id = writer && a.ids ? a.ids[row] : -1;
 
   Stat st{kLowest, 0.f, 0.f};
   {
     float2 s2 = make_float2(0.f, 0.f), t2 = s2;
     const int whole_end = static_cast<int>((static_cast<long long>(a.V) + r.shift) / N);
-    int u = rank * kLpThreads + static_cast<int>(threadIdx.x);
+    int u = rank * 32 * W + warp * 32 + lane;
     if (r.shift == 0 || u > 0) {
       const uint4 *src = reinterpret_cast<const uint4 *>(r.p - r.shift);  // vector 0, of which 0 .. shift - 1 is not ours
       for (; u + (kBatch - 1) * stride < whole_end; u += kBatch * stride) {
@@ -464,12 +486,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs(const LpArgs a) 
     st.s = s2.x + s2.y;
     st.t = t2.x + t2.y;
   }
-  const float best = st.s > 0.f ? st.m : -INFINITY;  // this thread's maximum
-  if constexpr (TOP) maxima[warp][lane] = warp_sort(ord_of(best), lane);
-  Stat all = block_stats(st, sm, warp, lane);
-  float bar = -INFINITY;
+  const float x_id = writer ? given_logit(a, r, id) : 0.f;  // not needed before the sums are joined
+  const float best = st.s > 0.f ? st.m : -INFINITY;          // this thread's maximum
+  uint32_t sorted = 0;
   if constexpr (TOP) {
-    if (warp == 0) s_best[lane] = merge_top(&maxima[0][0], a.top, lane);
+    sorted = warp_sort(ord_of(best), lane);
+    if (W > 1) maxima[warp][lane] = sorted;
+  }
+  Stat all = row_stats<W>(st, sm, warp, lane);
+  float bar = -INFINITY;
+  if constexpr (TOP && W > 1) {
+    if (warp == 0) s_best[lane] = merge_top<W>(&maxima[0][0], a.top, lane);
   }
   if constexpr (CLUSTER) {
     if (threadIdx.x == 0) {
@@ -503,19 +530,23 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs(const LpArgs a) 
       if (warp < C) maxima[warp][lane] = ld_cluster_u32(mapa_shared(smem_u32(&s_best[lane]), warp));
       if (warp >= C) maxima[warp][lane] = 0;
       __syncthreads();
-      bar = ord_value(__shfl_sync(0xffffffffu, merge_top(&maxima[0][0], a.top, lane), a.top - 1));
+      bar = ord_value(__shfl_sync(0xffffffffu, merge_top<W>(&maxima[0][0], a.top, lane), a.top - 1));
     }
-  } else if constexpr (TOP) {
+  } else if constexpr (TOP && W > 1) {
     __syncthreads();
     bar = ord_value(s_best[a.top - 1]);
+  } else if constexpr (TOP) {
+    bar = ord_value(__shfl_sync(0xffffffffu, sorted, a.top - 1));
   }
   const RowResult res(all);
   if (writer) write_row(a, row, res, id, x_id);
   if constexpr (TOP) {
-    lists[warp][lane] = select_top(r, rank * kLpThreads + warp * 32, stride, best, bar, lane);
-    __syncthreads();
-    uint64_t key = 0;
-    if (warp == 0) key = merge_top(&lists[0][0], a.top, lane);
+    uint64_t key = select_top(r, rank * 32 * W + warp * 32, stride, best, bar, lane);
+    if constexpr (W > 1) {
+      lists[warp][lane] = key;
+      __syncthreads();
+      if (warp == 0) key = merge_top<W>(&lists[0][0], a.top, lane);
+    }
     if constexpr (CLUSTER) {
       if (warp == 0) s_top[lane] = key;
       __syncwarp();
@@ -526,7 +557,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs(const LpArgs a) 
         else
           lists[warp][lane] = 0;
         __syncthreads();
-        if (warp == 0) key = merge_top(&lists[0][0], a.top, lane);
+        if (warp == 0) key = merge_top<W>(&lists[0][0], a.top, lane);
       }
     }
     if (rank == 0 && warp == 0 && lane < a.top) write_top(a, row, res, key, lane);
@@ -539,18 +570,31 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs(const LpArgs a) 
 
 template <typename T, bool TOP>
 avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
-  // few rows: several blocks a row, as long as each thread still has a vector
   const int sms = sm_count();
   const long long vecs = (a.V + Vec<T>::N - 1) / Vec<T>::N;
-  int C = 1;
-  while (C < 8 && static_cast<long long>(rows) * C * 2 <= 2ll * sms && vecs >= 2ll * C * kLpThreads) C *= 2;
-  a.blocks = C;
+  a.rows = rows;
+  a.blocks = 1;
+  // Few rows: several blocks a row, as long as a thread has four vectors and the
+  // blocks find room at once (1 x 50368 fp32: 9.8 us with one, 6.8 with eight;
+  // 300 rows: 14.8 with one, 20.6 with two).  Many rows: fewer warps to a row,
+  // whose ends cost less (6554 x 50368 bf16: 120 us with eight, 112 with four;
+  // 2000 x 2000: 10.4 with eight, 5.9 with four, 4.8 with one), unless a long
+  // row would be left to one warp at the end.
+  while (a.blocks < 8 && static_cast<long long>(rows) * a.blocks * 2 <= 2ll * sms && vecs >= 1024ll * a.blocks)
+    a.blocks *= 2;
+  const int C = a.blocks;
+  const int W = rows >= 8 * sms && vecs <= 1024 ? 1 : rows > 4 * sms || vecs <= 256 ? 4 : 8;
   if (C == 1) {
-    token_logprobs<T, TOP, false><<<rows, kLpThreads, 0, s>>>(a);
+    if (W == 1)
+      token_logprobs<T, TOP, 1, false><<<(rows + 3) / 4, 128, 0, s>>>(a);
+    else if (W == 4)
+      token_logprobs<T, TOP, 4, false><<<rows, 128, 0, s>>>(a);
+    else
+      token_logprobs<T, TOP, 8, false><<<rows, 256, 0, s>>>(a);
   } else {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * C);
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -559,7 +603,7 @@ avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, true>, static_cast<const LpArgs>(a));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, 8, true>, static_cast<const LpArgs>(a));
     if (e != cudaSuccess) {
       cudaGetLastError();
       set_detail("token_logprobs launch failed: %s", cudaGetErrorString(e));
