@@ -24,7 +24,7 @@ namespace {
 struct FewArgs {
   const void *x;
   long long ld_x;
-  int x_aligned, prenorm;
+  int x_fast, prenorm;
   const float *x_scale;
   int rows, N, K, stride;  // stride: bytes of a token in shared memory
   const int8_t *Wq;
@@ -45,41 +45,39 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 }
 
 // One row of x as 8-bit integers into shared memory (zeros behind K), by a warp.
-template <int DT>
+template <int DT, bool FAST>
 __device__ __forceinline__ void quantize_row_to(const FewArgs &a, int row, int8_t *dst, float *scale, int lane) {
-  const QuantSource<DT> src(a.x, row, a.rows, a.K, a.ld_x, a.x_aligned);
+  const QuantSource<DT, FAST> src(a.x, row, a.rows, a.K, a.ld_x);
   constexpr int kHold = 4;
   const int groups = a.stride / 8;
-  float v[kHold][8];
-  uint32_t mx = 0;
-  float ss = 0.f;
+  QuantRaw<DT> v[kHold];
+  QuantScan<DT, true> scan;
 #pragma unroll
   for (int i = 0; i < kHold; ++i) {
-    if (lane + 32 * i < groups) {
+    if (lane + 32 * i < groups)
       src.load(lane + 32 * i, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
+    else
+      v[i].clear();
   }
 #pragma unroll
-  for (int i = 0; i < kHold; ++i) quant_scan(v[i], mx, ss);
+  for (int i = 0; i < kHold; ++i) scan.add(v[i]);
   for (int g = lane + 32 * kHold; g < groups; g += 32) {
-    float t[8];
+    QuantRaw<DT> t;
     src.load(g, t);
-    quant_scan(t, mx, ss);
+    scan.add(t);
   }
-  mx = __reduce_max_sync(0xffffffffu, mx);
+  const uint32_t mx = __reduce_max_sync(0xffffffffu, scan.bits());
+  float ss = scan.squares();
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-  const RowScale rs(mx);
+  const RowScale rs(mx, false);
   if (lane == 0)
     *scale = a.prenorm ? rs.scale * (1.0f / sqrtf(ss / static_cast<float>(a.K) + 1e-6f)) : rs.scale;
 #pragma unroll
   for (int i = 0; i < kHold; ++i)
     if (lane + 32 * i < groups) *reinterpret_cast<uint2 *>(dst + (lane + 32 * i) * 8) = rs.quantize8(v[i]);
   for (int g = lane + 32 * kHold; g < groups; g += 32) {
-    float t[8];
+    QuantRaw<DT> t;
     src.load(g, t);
     *reinterpret_cast<uint2 *>(dst + g * 8) = rs.quantize8(t);
   }
@@ -124,7 +122,10 @@ __global__ void __launch_bounds__(WARPS * 32) linear_i8_few(const FewArgs a) {
       }
       if (lane == 0) xs[t] = a.x_scale[t];
     } else {
-      quantize_row_to<DT>(a, t, dst, xs + t, lane);
+      if (a.x_fast)
+        quantize_row_to<DT, true>(a, t, dst, xs + t, lane);
+      else
+        quantize_row_to<DT, false>(a, t, dst, xs + t, lane);
     }
   }
   __syncthreads();
@@ -244,7 +245,7 @@ avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, ave
   FewArgs a{};
   a.x = x;
   a.ld_x = ld_x;
-  a.x_aligned = x_dt != AVEY_I8 && quant_rows_aligned(x, x_dt, rows, ld_x);
+  a.x_fast = x_dt != AVEY_I8 && quant_rows_fast(x, x_dt, rows, p->K, ld_x);
   a.prenorm = prenorm;
   a.x_scale = x_scale;
   a.rows = rows;

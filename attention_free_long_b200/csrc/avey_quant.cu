@@ -4,8 +4,7 @@
 //   scale = s, or s / sqrt(mean(x^2) + 1e-6) with prenorm
 // One read of x and one write of q: HBM-bound (5 bytes a value from fp32, 3
 // from bf16).  A row stays in registers between the maximum and the rounding
-// (32 values a thread); only rows longer than 1024 values a warp, or 8192 a
-// block, are read again.
+// (32 values a thread); only rows longer than 8192 values are read again.
 #include <algorithm>
 
 #include "avey_common.cuh"
@@ -17,45 +16,45 @@ namespace {
 
 constexpr int kGroups = 4;  // groups of 8 values a thread keeps in registers
 
-// WPR warps per row: one when rows are short and many, eight otherwise.
-template <int DT, int WPR>
+// LPR threads per row: as few as hold it.
+template <int DT, int LPR, bool PRENORM, bool FAST>
 __global__ void __launch_bounds__(256) quantize_rows(const void *__restrict__ x, int rows, int cols,
-                                                     long long ld_x, int aligned, int prenorm,
-                                                     int8_t *__restrict__ q, long long ld_q,
-                                                     float *__restrict__ scale) {
-  constexpr int RPB = 8 / WPR;  // rows per block
+                                                     long long ld_x, int8_t *__restrict__ q,
+                                                     long long ld_q, float *__restrict__ scale) {
+  constexpr int RPB = 256 / LPR, WPR = LPR / 32;  // rows per block, warps per row
   __shared__ uint32_t s_max[8];
   __shared__ float s_sum[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * RPB + warp / WPR;
+  const int me = threadIdx.x % LPR;
+  const long long row = static_cast<long long>(blockIdx.x) * RPB + threadIdx.x / LPR;
   const bool live = row < rows;
-  const int step = 32 * WPR, me = (warp % WPR) * 32 + lane;
   const int groups = live ? ((cols + 15) / 16) * 2 : 0;  // up to roundup16(cols)
-  const QuantSource<DT> src(x, live ? row : 0, rows, cols, ld_x, aligned);
+  const QuantSource<DT, FAST> src(x, live ? row : 0, rows, cols, ld_x);
 
-  float v[kGroups][8];
-  uint32_t mx = 0;
-  float ss = 0.f;
+  QuantRaw<DT> v[kGroups];
+  QuantScan<DT, PRENORM> scan;
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
-    const int g = me + i * step;
-    if (g < groups) {
+    const int g = me + i * LPR;
+    if (g < groups)
       src.load(g, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
+    else
+      v[i].clear();
   }
 #pragma unroll
-  for (int i = 0; i < kGroups; ++i) quant_scan(v[i], mx, ss);
-  for (int g = me + kGroups * step; g < groups; g += step) {
-    float t[8];
+  for (int i = 0; i < kGroups; ++i) scan.add(v[i]);
+  for (int g = me + kGroups * LPR; g < groups; g += LPR) {
+    QuantRaw<DT> t;
     src.load(g, t);
-    quant_scan(t, mx, ss);
+    scan.add(t);
   }
-  mx = __reduce_max_sync(0xffffffffu, mx);
+  uint32_t mx = scan.bits();
+  float ss = scan.squares();
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  for (int off = (LPR < 32 ? LPR : 32) / 2; off > 0; off >>= 1) {
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    if (PRENORM) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  }
   if constexpr (WPR > 1) {
     if (lane == 0) {
       s_max[warp] = mx;
@@ -71,39 +70,52 @@ __global__ void __launch_bounds__(256) quantize_rows(const void *__restrict__ x,
     }
   }
   if (!live) return;
-  const RowScale rs(mx);
+  const RowScale rs(mx, DT == AVEY_BF16);
   if (me == 0)
-    scale[row] = prenorm ? rs.scale * (1.0f / sqrtf(ss / static_cast<float>(cols) + 1e-6f)) : rs.scale;
+    scale[row] = PRENORM ? rs.scale * (1.0f / sqrtf(ss / static_cast<float>(cols) + 1e-6f)) : rs.scale;
   int8_t *qr = q + row * ld_q;
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
-    const int g = me + i * step;
+    const int g = me + i * LPR;
     if (g < groups) *reinterpret_cast<uint2 *>(qr + g * 8ll) = rs.quantize8(v[i]);
   }
-  for (int g = me + kGroups * step; g < groups; g += step) {
-    float t[8];
+  for (int g = me + kGroups * LPR; g < groups; g += LPR) {
+    QuantRaw<DT> t;
     src.load(g, t);
     *reinterpret_cast<uint2 *>(qr + g * 8ll) = rs.quantize8(t);
   }
 }
 
+template <int DT, bool PRENORM, bool FAST>
+avey_status run_quantize(const void *x, int rows, int cols, long long ld_x, int8_t *q, long long ld_q,
+                         float *scale, cudaStream_t s) {
+#define AVEY_QUANTIZE(LPR) \
+  quantize_rows<DT, LPR, PRENORM, FAST><<<(rows + 256 / LPR - 1) / (256 / LPR), 256, 0, s>>>(x, rows, cols, ld_x, q, ld_q, scale)
+  // a thread holds 32 values; with fewer rows than SMs a block per row spreads
+  // the loads of a row
+  if (cols > 128 * 32 || (rows <= sm_count() && cols > 256))
+    AVEY_QUANTIZE(256);
+  else if (cols > 64 * 32)
+    AVEY_QUANTIZE(128);
+  else if (cols > 32 * 32)
+    AVEY_QUANTIZE(64);
+  else if (cols > 8 * 32)
+    AVEY_QUANTIZE(32);
+  else
+    AVEY_QUANTIZE(8);
+#undef AVEY_QUANTIZE
+  AVEY_CHECK_LAUNCH("quantize_rows", s);
+  return AVEY_OK;
+}
+
 template <int DT>
 avey_status run_quantize(const void *x, int rows, int cols, long long ld_x, int prenorm, int8_t *q,
                          long long ld_q, float *scale, cudaStream_t s) {
-  const int al = quant_rows_aligned(x, DT, rows, ld_x) ? 1 : 0;
-  // as few warps a row as hold it (1024 values each); with fewer rows than SMs
-  // eight, which spreads the loads of a row
-  constexpr int kHold = kGroups * 256;
-  if (cols > 4 * kHold || rows <= sm_count())
-    quantize_rows<DT, 8><<<rows, 256, 0, s>>>(x, rows, cols, ld_x, al, prenorm, q, ld_q, scale);
-  else if (cols > 2 * kHold)
-    quantize_rows<DT, 4><<<(rows + 1) / 2, 256, 0, s>>>(x, rows, cols, ld_x, al, prenorm, q, ld_q, scale);
-  else if (cols > kHold)
-    quantize_rows<DT, 2><<<(rows + 3) / 4, 256, 0, s>>>(x, rows, cols, ld_x, al, prenorm, q, ld_q, scale);
-  else
-    quantize_rows<DT, 1><<<(rows + 7) / 8, 256, 0, s>>>(x, rows, cols, ld_x, al, prenorm, q, ld_q, scale);
-  AVEY_CHECK_LAUNCH("quantize_rows", s);
-  return AVEY_OK;
+  if (quant_rows_fast(x, DT, rows, cols, ld_x))
+    return prenorm ? run_quantize<DT, true, true>(x, rows, cols, ld_x, q, ld_q, scale, s)
+                   : run_quantize<DT, false, true>(x, rows, cols, ld_x, q, ld_q, scale, s);
+  return prenorm ? run_quantize<DT, true, false>(x, rows, cols, ld_x, q, ld_q, scale, s)
+                 : run_quantize<DT, false, false>(x, rows, cols, ld_x, q, ld_q, scale, s);
 }
 
 }  // namespace

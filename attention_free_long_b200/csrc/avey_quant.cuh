@@ -7,24 +7,58 @@
 
 namespace avey {
 
-// Whether every row of x (both planes of a pair) starts on a 16-byte boundary.
-inline bool quant_rows_aligned(const void *x, int dt, long long rows, long long ld) {
+// Whether every row of x (both planes of a pair) is whole groups of 8 values on
+// 16-byte boundaries.
+inline bool quant_rows_fast(const void *x, int dt, long long rows, int cols, long long ld) {
   const long long es = dt == AVEY_F32 ? 4 : 2;
-  return aligned16(x) && (ld * es) % 16 == 0 && (dt != AVEY_BF16X2 || (rows * ld * es) % 16 == 0);
+  return cols % 8 == 0 && aligned16(x) && (ld * es) % 16 == 0 && (dt != AVEY_BF16X2 || (rows * ld * es) % 16 == 0);
 }
 
-// One row of x, in groups of 8 consecutive values; values past the row's end
-// are 0.
+// Eight consecutive values of a row as they lie in memory.
 template <int DT>
+struct QuantRaw {
+  uint4 w[DT == AVEY_BF16 ? 1 : 2];  // fp32: two words; pair: hi and lo
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (auto &x : w) x = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if constexpr (DT == AVEY_F32) {
+      const uint32_t a[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(a[i]);
+    } else {
+      const uint32_t a[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(a[i] << 16);
+        v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+      }
+      if constexpr (DT == AVEY_BF16X2) {
+        const uint32_t b[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 t = fadd2(make_float2(v[2 * i], v[2 * i + 1]),
+                                 make_float2(__uint_as_float(b[i] << 16), __uint_as_float(b[i] & 0xffff0000u)));
+          v[2 * i] = t.x;
+          v[2 * i + 1] = t.y;
+        }
+      }
+    }
+  }
+};
+
+// One row of x, in groups of 8 consecutive values; values past the row's end
+// are 0.  FAST: rows of whole groups on 16-byte boundaries.
+template <int DT, bool FAST>
 struct QuantSource {
   const float *f = nullptr;
   const bf16 *h = nullptr, *l = nullptr;
   int cols;
-  bool aligned;
 
-  __device__ __forceinline__ QuantSource(const void *x, long long row, long long rows, int cols_,
-                                         long long ld, int aligned_)
-      : cols(cols_), aligned(aligned_ != 0) {
+  __device__ __forceinline__ QuantSource(const void *x, long long row, long long rows, int cols_, long long ld)
+      : cols(cols_) {
     if constexpr (DT == AVEY_F32) {
       f = static_cast<const float *>(x) + row * ld;
     } else {
@@ -33,74 +67,103 @@ struct QuantSource {
     }
   }
 
-  __device__ __forceinline__ void load(int g, float (&v)[8]) const {
+  __device__ __forceinline__ void load(int g, QuantRaw<DT> &r) const {
     const int c = g * 8;
-    if (aligned && c + 8 <= cols) {
-      if constexpr (DT == AVEY_F32) {
-        const float4 a = *reinterpret_cast<const float4 *>(f + c);
-        const float4 b = *reinterpret_cast<const float4 *>(f + c + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    if constexpr (FAST) {
+      if (c >= cols) {
+        r.clear();
+      } else if constexpr (DT == AVEY_F32) {
+        r.w[0] = *reinterpret_cast<const uint4 *>(f + c);
+        r.w[1] = *reinterpret_cast<const uint4 *>(f + c + 4);
       } else {
-        const uint4 a = *reinterpret_cast<const uint4 *>(h + c);
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 p = unpack_bf16(aw[i]);
-          v[2 * i] = p.x;
-          v[2 * i + 1] = p.y;
-        }
-        if constexpr (DT == AVEY_BF16X2) {
-          const uint4 b = *reinterpret_cast<const uint4 *>(l + c);
-          const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 p = unpack_bf16(bw[i]);
-            v[2 * i] += p.x;
-            v[2 * i + 1] += p.y;
-          }
-        }
+        r.w[0] = *reinterpret_cast<const uint4 *>(h + c);
+        if constexpr (DT == AVEY_BF16X2) r.w[1] = *reinterpret_cast<const uint4 *>(l + c);
       }
     } else {
+      uint32_t b[8] = {};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[i] = 0.f;
-        if (c + i < cols) {
-          if constexpr (DT == AVEY_F32) {
-            v[i] = f[c + i];
-          } else {
-            v[i] = __bfloat162float(h[c + i]);
-            if constexpr (DT == AVEY_BF16X2) v[i] += __bfloat162float(l[c + i]);
-          }
+        if (c + i >= cols) continue;
+        if constexpr (DT == AVEY_F32) {
+          b[i] = __float_as_uint(f[c + i]);
+        } else {
+          b[i / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(h[c + i])) << (16 * (i & 1));
+          if constexpr (DT == AVEY_BF16X2)
+            b[4 + i / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(l[c + i])) << (16 * (i & 1));
         }
       }
+      r.w[0] = make_uint4(b[0], b[1], b[2], b[3]);
+      if constexpr (DT != AVEY_BF16) r.w[1] = make_uint4(b[4], b[5], b[6], b[7]);
     }
   }
 };
 
-// Running maximum of |x| as its bit pattern (which orders NaN above infinity
-// above every finite value) and sum of squares.
-__device__ __forceinline__ void quant_scan(const float (&v)[8], uint32_t &mx, float &ss) {
+// Running maximum of |x| and what tells whether any value is not finite; with
+// SQ the sum of squares.
+template <int DT, bool SQ>
+struct QuantScan {
+  float mx = 0.f;               // bf16: unused
+  float2 chk = {0.f, 0.f};      // NaN once a value was not finite; bf16: unused
+  uint32_t m2 = 0;              // bf16: maxima of the two halves' bits, which order NaN above infinity
+  float2 ss = {0.f, 0.f};
+
+  __device__ __forceinline__ void add(const QuantRaw<DT> &r) {
+    float v[8];
+    if (DT != AVEY_BF16 || SQ) r.values(v);
+    if constexpr (DT == AVEY_BF16) {
+      const uint32_t a[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    mx = max(mx, __float_as_uint(v[j]) & 0x7fffffffu);
-    ss = fmaf(v[j], v[j], ss);
+      for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, a[i] & 0x7fff7fffu);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        mx = fmaxf(fmaxf(mx, fabsf(v[i])), fabsf(v[i + 1]));
+        chk = ffma2(make_float2(v[i], v[i + 1]), make_float2(0.f, 0.f), chk);
+      }
+    }
+    if constexpr (SQ) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) ss = ffma2(make_float2(v[i], v[i + 1]), make_float2(v[i], v[i + 1]), ss);
+    }
   }
-}
+  // Bits of the largest |x|, at least those of infinity if one is not finite.
+  __device__ __forceinline__ uint32_t bits() const {
+    if constexpr (DT == AVEY_BF16) {
+      const uint32_t m = max(m2 & 0xffffu, m2 >> 16) << 16;
+      return m;
+    } else {
+      return chk.x == 0.f && chk.y == 0.f ? __float_as_uint(mx) : 0x7f800000u;
+    }
+  }
+  __device__ __forceinline__ float squares() const { return ss.x + ss.y; }
+};
 
 // The scale of a row from the bits of its largest magnitude, and the rounding.
 struct RowScale {
   float scale;  // s; NaN for a row that is not finite
   float s, inv;
   bool zero, slow;
+  static constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
 
-  __device__ __forceinline__ explicit RowScale(uint32_t max_bits) {
+  // short_values: x has so few bits that half the largest value, 63.5 steps to
+  // within rounding, is met often.  inv is then moved by an ulp or two until the
+  // fast rounding of that value is right.
+  __device__ __forceinline__ RowScale(uint32_t max_bits, bool short_values) {
     const bool bad = max_bits >= 0x7f800000u;
     s = __fmul_rn(__uint_as_float(max_bits), 1.0f / 127.0f);
     scale = bad ? __uint_as_float(0x7fc00000u) : s;
     zero = bad || s == 0.0f;
     slow = s < 1e-30f;  // 1 / s may overflow
     inv = 1.0f / s;
+    if (short_values && !zero && !slow) {
+      const float h = 0.5f * __uint_as_float(max_bits), r = fmaf(-63.0f, s, h);
+      const bool up = 2.0f * r >= s;  // 64 is even: it takes the tie
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const bool got = fmaf(h, inv, kMagic) - kMagic == 64.0f;
+        if (got != up) inv = __uint_as_float(__float_as_uint(inv) + (up ? 1u : ~0u));
+      }
+    }
   }
 
   // RNE of the exact x / s, tie to even.  The remainder r = x - q s is exact in
@@ -116,30 +179,44 @@ struct RowScale {
     return static_cast<int>(fminf(fmaxf(q, -127.0f), 127.0f));
   }
 
-  // Eight values.  x * inv + 1.5 * 2^23 rounds to a whole number whose low byte
-  // is q; inv is off by a few ulp, so q may be wrong next to a half, where
-  // 2 |r| reaches s: then (and for scales whose inverse overflows) all eight
-  // take the exact form.
-  __device__ __forceinline__ uint2 quantize8(const float (&v)[8]) const {
+  // Eight values.  The low byte of x * inv + 1.5 * 2^23 is q; inv is off by a
+  // few ulp, so q may be off by one next to a half, where 2 |r| reaches s, and is
+  // put right there.  Scales whose inverse overflows take the division.
+  template <int DT>
+  __device__ __forceinline__ uint2 quantize8(const QuantRaw<DT> &raw) const {
+    float v[8];
+    raw.values(v);
     if (zero) return make_uint2(0u, 0u);
-    constexpr float kMagic = 12582912.0f;
     uint32_t b[8];
     float far = 0.f;
+    const float2 inv2 = make_float2(inv, inv), m2 = make_float2(kMagic, kMagic);
+    const float2 minus_m = make_float2(-kMagic, -kMagic), minus_s = make_float2(-s, -s);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float t = fmaf(v[j], inv, kMagic);
-      b[j] = __float_as_uint(t);
-      far = fmaxf(far, fabsf(fmaf(kMagic - t, s, v[j])));
+    for (int j = 0; j < 8; j += 2) {
+      const float2 x = make_float2(v[j], v[j + 1]);
+      const float2 t = ffma2(x, inv2, m2);
+      const float2 r = ffma2(fadd2(t, minus_m), minus_s, x);
+      b[j] = __float_as_uint(t.x);
+      b[j + 1] = __float_as_uint(t.y);
+      far = fmaxf(fmaxf(far, fabsf(r.x)), fabsf(r.y));
     }
-    if (slow || far * 2.0f >= s) {
-#pragma unroll 1
+    if (far * 2.0f >= s || slow) {
+#pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float x = v[0];
+        const float t = __uint_as_float(b[j]);
+        const float r = fmaf(kMagic - t, s, v[j]), r2 = fabsf(r) * 2.0f;
+        if (r2 > s || (r2 == s && (b[j] & 1u))) b[j] = __float_as_uint(t + copysignf(1.0f, r));
+      }
+      if (slow) {
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+          float x = v[0];
 #pragma unroll
-        for (int q = 1; q < 8; ++q) x = q == j ? v[q] : x;
-        const uint32_t e = static_cast<uint32_t>(exact(x));
+          for (int q = 1; q < 8; ++q) x = q == j ? v[q] : x;
+          const uint32_t e = static_cast<uint32_t>(exact(x));
 #pragma unroll
-        for (int q = 0; q < 8; ++q) b[q] = q == j ? e : b[q];
+          for (int q = 0; q < 8; ++q) b[q] = q == j ? e : b[q];
+        }
       }
     }
     uint32_t w[2];
