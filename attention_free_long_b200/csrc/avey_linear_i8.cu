@@ -2,10 +2,15 @@
 // (kind::i8, int32 accumulators in TMEM).
 //
 // CTA pairs (cta_group::2) own 256 x BN output tiles; roles and barriers are
-// those of the layer GEMMs (avey_tc.cu): a TMA producer warp, one thread of
-// CTA 0 issuing the MMAs, four epilogue warps per CTA, two accumulators so
-// that the epilogue of a tile overlaps the MMAs of the next.  A K step is 128
-// bytes = 128 values, four MMAs of K = 32.
+// those of the layer GEMMs (avey_tc.cu): a TMA producer warp, a warp of CTA 0
+// issuing the MMAs, epilogue warps, two accumulators so that the epilogue of a
+// tile overlaps the MMAs of the next.  A K step is 128 bytes = 128 values, four
+// MMAs of K = 32.
+//
+// What bounds it: an SM takes about 41 bytes a cycle from L2, and a 256 x 256
+// tile needs 64 (32 KB a K step of 512 cycles): 8192^3 runs at 3.0 POP/s.  Up to
+// K = 1024 a pair therefore keeps its 256 rows of x in shared memory and walks
+// the channels (ARES), which halves that; then the epilogue bounds.
 #include <algorithm>
 
 #include "avey_common.cuh"
@@ -15,7 +20,7 @@ namespace avey {
 namespace {
 
 constexpr int kBK = 128;
-constexpr int kLinEpi = 16, kGroups = kLinEpi / 4, kLinThreads = 64 + 32 * kLinEpi;
+constexpr int kResidentSteps = 8;  // K steps of x that fit beside a ring
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar2 = -200.0f;  // ex2 is 0 in fp32 from here down
@@ -45,27 +50,40 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // AVEY_BF16X2 (stores): running softmax statistics of each row.
 constexpr int kScore = -1;
 
-template <int BN, int OUT>
+template <int BN, int OUT, bool RES, bool ARES>
 struct LinLayout {
   static constexpr int PM = 256;
-  static constexpr uint32_t A_BYTES = 128 * kBK;        // this CTA's rows
+  static constexpr int EPI = OUT == kScore ? 16 : 8;    // epilogue warps
+  static constexpr int GROUPS = EPI / 4;                // warps that share a quarter's chunks
+  static constexpr int THREADS = 64 + 32 * EPI;
+  static constexpr uint32_t A_BYTES = 128 * kBK;        // this CTA's rows, one K step
   static constexpr uint32_t B_BYTES = (BN / 2) * kBK;   // this CTA's half of the channels
-  static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr uint32_t STAGE_BYTES = ARES ? B_BYTES : A_BYTES + B_BYTES;
+  // staging of stores (and of the residual, fetched a chunk ahead): a 32 x 32
+  // chunk a buffer
   static constexpr uint32_t BUF = OUT == kScore ? 0 : OUT == AVEY_BF16 ? 2048 : 4096;
-  static constexpr int BUFS = OUT == AVEY_BF16 ? 2 : 1;
-  static constexpr int STAGES = OUT == kScore ? 6 : BN < 256 ? 6 : 4;
-  static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES;
+  static constexpr int BUFS = RES ? 3 : OUT == AVEY_BF16 ? 2 : 1;
+  static constexpr uint32_t STAGING_BYTES = EPI * BUFS * BUF;
   static constexpr uint32_t CTRL_BYTES = 1024;
-  static constexpr uint32_t COLS_BYTES = kLinEpi * 2 * 32 * 4;  // each warp's scale and bias
-  static constexpr uint32_t STAGING_BYTES = kLinEpi * BUFS * BUF;
-  static constexpr uint32_t SMEM_BYTES = TILES_BYTES + STAGING_BYTES + CTRL_BYTES + COLS_BYTES + 1024;
+  static constexpr uint32_t COLS_BYTES = EPI * 2 * 32 * 4;  // each warp's scale and bias
+  static constexpr uint32_t REST_BYTES = STAGING_BYTES + CTRL_BYTES + COLS_BYTES + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
-  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-  static_assert(STAGES <= 8, "the control block holds at most 8 stages");
+  // stages and shared memory for this many K steps
+  static constexpr int stages(int ksteps) {
+    const uint32_t room = 232448 - REST_BYTES - (ARES ? ksteps * A_BYTES : 0);
+    const int n = static_cast<int>(room / STAGE_BYTES);
+    return n < 8 ? n : 8;
+  }
+  static constexpr uint32_t tiles_bytes(int ksteps) {
+    return (ARES ? ksteps * A_BYTES : 0) + stages(ksteps) * STAGE_BYTES;
+  }
+  static_assert(stages(ARES ? kResidentSteps : 1) >= 3, "shared memory budget");
 };
 
 struct LinArgs {
   int rows, N, K;
+  int stages;            // of the ring
+  uint32_t tiles_bytes;  // resident rows and ring
   int tiles_m, tiles_n;
   long long num_tiles;
   const float *x_scale, *w_scale, *bias;
@@ -117,11 +135,11 @@ __device__ __forceinline__ void lin_st4(uint32_t addr, uint32_t a, uint32_t b, u
                : "memory");
 }
 
-// Four consecutive fp32 of a residual row of n, zeros past its end (plain
-// loads: the call may overwrite it).
-__device__ __forceinline__ float4 load4_rw(const float *p, int i, int n) {
-  if (i + 4 <= n) return *reinterpret_cast<const float4 *>(p + i);
-  return make_float4(i < n ? p[i] : 0.f, i + 1 < n ? p[i + 1] : 0.f, i + 2 < n ? p[i + 2] : 0.f, 0.f);
+__device__ __forceinline__ void ld_shared4(uint32_t addr, float (&r)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -140,14 +158,14 @@ __device__ __forceinline__ void rebase2(Stat2 &a, float M) {
   a.m = M;
 }
 
-// First tile of pair p's share of the scoring: shares are contiguous in the
-// order (row block, word block).
-__host__ __device__ __forceinline__ long long score_start(long long p, long long tiles, int npairs) {
+// First tile of pair p's share: shares are contiguous in the order (row block,
+// column block).
+__host__ __device__ __forceinline__ long long share_start(long long p, long long tiles, int npairs) {
   return p * tiles / npairs;
 }
 
-// The columns from N_tma of a row's 32-column chunk.
-template <int OUT>
+// The columns from N_tma of a row's 32-column chunk, residual included.
+template <int OUT, bool RES>
 __device__ __forceinline__ void store_rest(const LinArgs &a, int row, int col0, const float (&v)[32]) {
   const long long at = static_cast<long long>(row) * a.ld_out;
 #pragma unroll
@@ -155,7 +173,7 @@ __device__ __forceinline__ void store_rest(const LinArgs &a, int row, int col0, 
     const int c = col0 + j;
     if (c < a.N_tma || c >= a.N) continue;
     if constexpr (OUT == AVEY_F32) {
-      static_cast<float *>(a.out)[at + c] = v[j];
+      static_cast<float *>(a.out)[at + c] = RES ? v[j] + a.residual[at + c] : v[j];
     } else {
       bf16 *hi = static_cast<bf16 *>(a.out) + at + c;
       *hi = __float2bfloat16_rn(v[j]);
@@ -172,20 +190,28 @@ __device__ __forceinline__ void store_rest(const LinArgs &a, int row, int col0, 
 // the chunk's columns in shared memory.
 __device__ __forceinline__ void lin_values(float (&v)[32], float xs, const float *w, const float *b,
                                            int relu2) {
+  const float2 x2 = make_float2(xs, xs);
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     const float4 w4 = *reinterpret_cast<const float4 *>(w + 4 * q);
     const float4 b4 = *reinterpret_cast<const float4 *>(b + 4 * q);
-    const float ww[4] = {w4.x, w4.y, w4.z, w4.w}, bb[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[4 * q + j] = fmaf(static_cast<float>(__float_as_int(v[4 * q + j])) * xs, ww[j], bb[j]);
+    for (int h = 0; h < 2; ++h) {
+      const float2 f = make_float2(static_cast<float>(__float_as_int(v[4 * q + 2 * h])),
+                                   static_cast<float>(__float_as_int(v[4 * q + 2 * h + 1])));
+      const float2 y = ffma2(fmul2(f, x2), h ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y),
+                             h ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y));
+      v[4 * q + 2 * h] = y.x;
+      v[4 * q + 2 * h + 1] = y.y;
+    }
   }
   if (relu2) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float y = max_nan(v[j], 0.f);  // NaN stays NaN
-      v[j] = y * y;
+    for (int j = 0; j < 32; j += 2) {
+      const float2 y = make_float2(max_nan(v[j], 0.f), max_nan(v[j + 1], 0.f));  // NaN stays NaN
+      const float2 z = fmul2(y, y);
+      v[j] = z.x;
+      v[j + 1] = z.y;
     }
   }
 }
@@ -222,20 +248,25 @@ __device__ __forceinline__ void score_values(float (&v)[32], float xs, const flo
   st.t += t.x + t.y;
 }
 
-template <int BN, int OUT, bool RES>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
+template <int BN, int OUT, bool RES, bool ARES>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, RES, ARES>::THREADS, 1)
     linear_i8_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
-                   const LinArgs a) {
-  using P = LinLayout<BN, OUT>;
+                   const __grid_constant__ CUtensorMap tmR, const LinArgs a) {
+  using P = LinLayout<BN, OUT, RES, ARES>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
-  uint8_t *ctrl = smem_raw + pad + P::TILES_BYTES + P::STAGING_BYTES;
-  const uint32_t sbase = raw_s + pad;
-  const uint32_t cbase = sbase + P::TILES_BYTES + P::STAGING_BYTES;
+  const int kchunks = (a.K + kBK - 1) / kBK;
+  // shared memory: resident rows (ARES), ring, staging, control block, columns
+  const uint32_t abase = raw_s + pad;
+  const uint32_t sbase = abase + (ARES ? static_cast<uint32_t>(kchunks) * P::A_BYTES : 0u);
+  const uint32_t gbase = abase + a.tiles_bytes;
+  const uint32_t cbase = gbase + P::STAGING_BYTES;
+  uint8_t *ctrl = smem_raw + pad + a.tiles_bytes + P::STAGING_BYTES;
   // control block: full[8] @0, empty[8] @64, tfull[2] @128, tempty[2] @144,
-  // drain @160, tmem base @168, abort flag @172
+  // drain @160, tmem base @168, abort flag @172, afull[8] @192, aempty[8] @256,
+  // residual[8 warps][3] @320
   auto full_bar = [&](int s) { return cbase + 8u * s; };
   auto empty_bar = [&](int s) { return cbase + 64u + 8u * s; };
   auto tfull_bar = [&](int i) { return cbase + 128u + 8u * i; };
@@ -243,26 +274,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   const uint32_t drain_bar = cbase + 160u;
   volatile uint32_t *tmem_holder = reinterpret_cast<volatile uint32_t *>(ctrl + 168);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 172);
+  auto afull_bar = [&](int k) { return cbase + 192u + 8u * k; };
+  auto aempty_bar = [&](int k) { return cbase + 256u + 8u * k; };
+  auto res_bar = [&](int w, int i) { return cbase + 320u + 24u * w + 8u * i; };
+  static_assert(320 + 24 * 8 <= P::CTRL_BYTES && kResidentSteps <= 8, "control block");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  // Tiles of this pair: dealt round robin, or for the scores a contiguous
-  // share, so that a row's statistics stay in one thread's registers.
-  const long long t_first = OUT == kScore ? score_start(pair, a.num_tiles, npairs) : pair;
-  const long long t_end = OUT == kScore ? score_start(pair + 1, a.num_tiles, npairs) : a.num_tiles;
-  const long long t_step = OUT == kScore ? 1 : npairs;
+  // Tiles of this pair: dealt round robin, or a contiguous share, so that rows
+  // stay in shared memory and a row's statistics in one thread's registers.
+  constexpr bool SHARE = ARES || OUT == kScore;
+  const long long t_first = SHARE ? share_start(pair, a.num_tiles, npairs) : pair;
+  const long long t_end = SHARE ? share_start(pair + 1, a.num_tiles, npairs) : a.num_tiles;
+  const long long t_step = SHARE ? 1 : npairs;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < P::STAGES; ++s) {
+    for (int s = 0; s < a.stages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull_bar(i), 1);
-      mbar_init(tempty_bar(i), 2 * kLinEpi);
+      mbar_init(tempty_bar(i), 2 * P::EPI);
     }
     mbar_init(drain_bar, 1);
+    if (ARES) {
+      for (int k = 0; k < kchunks; ++k) {
+        mbar_init(afull_bar(k), 1);
+        mbar_init(aempty_bar(k), 1);
+      }
+    }
+    if (RES) {
+      for (int w = 0; w < P::EPI; ++w)
+        for (int i = 0; i < P::BUFS; ++i) mbar_init(res_bar(w, i), 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -271,6 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     prefetch_tmap(&tmB);
     if (OUT != kScore) prefetch_tmap(&tmO0);
     if (OUT == AVEY_BF16X2) prefetch_tmap(&tmO1);
+    if (RES) prefetch_tmap(&tmR);
   }
   cluster_sync_all();
   if (warp == 1) {
@@ -281,22 +328,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int kchunks = (a.K + kBK - 1) / kBK;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     // The whole warp walks the loop, so that addresses stay in uniform
     // registers; one lane issues.
     const bool one = elect_one();
-    const uint32_t full0 = mapa_shared(full_bar(0), 0);
+    const uint32_t full0 = mapa_shared(full_bar(0), 0), afull0 = mapa_shared(afull_bar(0), 0);
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, aphase = 0;
     long long issued = 0;
-    bool ok = true;
+    bool ok = true, fresh = true;  // fresh: the pair's first tile of a row block
     for (TileWalk w(a, t_first, t_end, t_step); ok && w.more(); w.next()) {
       const int arow = w.mt * P::PM + static_cast<int>(rank) * 128;
       const int brow = w.nt * BN + static_cast<int>(rank) * (BN / 2);
+      fresh = fresh || w.nt == 0;
       for (int kc = 0; kc < kchunks; ++kc) {
+        if (ARES && fresh) {
+          if (!warp_wait(aempty_bar(kc), aphase ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (one) {
+            if (rank == 0) mbar_arrive_expect_tx(afull_bar(kc), 2 * P::A_BYTES);
+            tma_load_3d_pair(abase + kc * P::A_BYTES, &tmA, afull0 + 8u * kc, kc * kBK, arow, 0);
+          }
+        }
         if (!warp_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
           ok = false;
           break;
@@ -304,26 +361,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         const uint32_t st = sbase + stage * P::STAGE_BYTES, bar = full0 + 8u * stage;
         if (one) {
           if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * P::STAGE_BYTES);
-          tma_load_3d_pair(st, &tmA, bar, kc * kBK, arow, 0);
-          tma_load_3d_pair(st + P::A_BYTES, &tmB, bar, kc * kBK, brow, 0);
+          if (!ARES) tma_load_3d_pair(st, &tmA, bar, kc * kBK, arow, 0);
+          tma_load_3d_pair(ARES ? st : st + P::A_BYTES, &tmB, bar, kc * kBK, brow, 0);
         }
         ++issued;
-        if (++stage == P::STAGES) {
+        if (++stage == a.stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
+      if (ARES && fresh) aphase ^= 1u;
+      fresh = false;
     }
     if (one) {
       if (!ok) {
         *abort_flag = 1;
         record_status(a.status, AVEY_ERR_DEVICE_TIMEOUT);
       }
-      // Drain: a stage's last use is over once the pair's MMA has released it.
-      for (int s = 0; s < P::STAGES; ++s) {
+      // Drain: a stage's last use is over once the pair's MMA has released it
+      // (and with it every earlier read of the resident rows).
+      for (int s = 0; s < a.stages; ++s) {
         if (issued > s) {
-          const long long last = ((issued - 1 - s) / P::STAGES) * P::STAGES + s;
-          drain_wait(empty_bar(s), static_cast<uint32_t>((last / P::STAGES) & 1));
+          const long long last = ((issued - 1 - s) / a.stages) * a.stages + s;
+          drain_wait(empty_bar(s), static_cast<uint32_t>((last / a.stages) & 1));
         }
       }
     }
@@ -335,27 +395,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     if (rank == 0) {
       constexpr uint32_t idesc = idesc_s8_s32(P::PM, BN);
       const bool one = elect_one();
-      const long long tiles = t_first < t_end ? (t_end - t_first + t_step - 1) / t_step : 0;
       const int last_steps = (a.K - (kchunks - 1) * kBK + 31) / 32;  // MMAs of the last K step; the rest is zeros
-      const uint64_t desc0 = sdesc_k_sw128(sbase);
+      const uint64_t desc_a = sdesc_k_sw128(abase), desc_s = sdesc_k_sw128(sbase);
       int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (long long t = 0; ok && t < tiles; ++t) {
+      uint32_t phase = 0, acc_phase = 0, aphase = 0;
+      bool ok = true, fresh = true;
+      for (TileWalk w(a, t_first, t_end, t_step); ok && w.more();) {
         if (!warp_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        fresh = fresh || w.nt == 0;
+        const bool leave = w.nt == a.tiles_n - 1;  // the row block's last tile
+        w.next();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
         for (int kc = 0; kc < kchunks; ++kc) {
+          if (ARES && fresh && !warp_wait(afull_bar(kc), aphase, abort_flag)) {
+            ok = false;
+            break;
+          }
           if (!warp_wait(full_bar(stage), phase, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t da = desc0 + static_cast<uint32_t>(stage) * (P::STAGE_BYTES >> 4);
-          const uint64_t db = da + (P::A_BYTES >> 4);
+          const uint64_t ds = desc_s + static_cast<uint32_t>(stage) * (P::STAGE_BYTES >> 4);
+          const uint64_t da = ARES ? desc_a + static_cast<uint32_t>(kc) * (P::A_BYTES >> 4) : ds;
+          const uint64_t db = ARES ? ds : ds + (P::A_BYTES >> 4);
           const bool whole = kc + 1 < kchunks || last_steps == kBK / 32;
           if (one) {
             tc_mma_i8_pair(d_tmem, da, db, idesc, kc != 0);
@@ -367,14 +434,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 tc_mma_i8_pair(d_tmem, da + 2u * kk, db + 2u * kk, idesc, 1u);
             }
             tc_commit_pair_both(empty_bar(stage));
+            if (ARES && leave) tc_commit_pair_both(aempty_bar(kc));
             if (kc + 1 == kchunks) tc_commit_pair_both(tfull_bar(acc));
           }
           __syncwarp();
-          if (++stage == P::STAGES) {
+          if (++stage == a.stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
+        if (ARES && fresh) aphase ^= 1u;
+        fresh = false;
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
@@ -389,43 +459,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
   } else {
     // ------------------------------------------------------------- epilogue
-    // Sixteen warps: a quarter of the CTA's rows (TMEM lanes 32*quarter .. +31)
-    // and every fourth 32-column chunk each.  With eight the warps issued in a
-    // third of the cycles only, waiting for TMEM and for one another.
-    const int quarter = warp & 3, group = (warp - 2) >> 2;
-    const uint32_t stg = sbase + P::TILES_BYTES + static_cast<uint32_t>(warp - 2) * P::BUFS * P::BUF;
+    // A warp has a quarter of the CTA's rows (TMEM lanes 32*quarter .. +31) and
+    // every GROUPS-th 32-column chunk.
+    const int ew = warp - 2, quarter = warp & 3, group = ew >> 2;
+    const uint32_t stg = gbase + static_cast<uint32_t>(ew) * P::BUFS * P::BUF;
     const uint32_t tempty_r0 = mapa_shared(tempty_bar(0), 0), tempty_r1 = mapa_shared(tempty_bar(1), 0);
-    float *w_s = reinterpret_cast<float *>(ctrl + P::CTRL_BYTES) + (warp - 2) * 64, *b_s = w_s + 32;
-    // Scale and bias of this lane's column of a chunk, fetched a chunk ahead.
-    // The scores work in units of log 2, where words past the last have the
-    // value -1e30, as those with a bias below it (-inf among them): finite, so
-    // that 0 * (y - m) stays 0.
+    float *w_s = reinterpret_cast<float *>(ctrl + P::CTRL_BYTES) + ew * 64, *b_s = w_s + 32;
+    auto row_of = [&](int mt) { return mt * P::PM + static_cast<int>(rank) * 128 + quarter * 32; };
+    auto row_scale = [&](int mt) {
+      const int row = row_of(mt) + lane;
+      return row < a.rows ? __ldg(a.x_scale + row) * (OUT == kScore ? kLog2e : 1.f) : 0.f;
+    };
+    // Fetches, a chunk ahead, scale and bias of this lane's column of a chunk,
+    // and the chunk's residual into staging buffer `buf`.  The scores work in
+    // units of log 2, where words past the last have the value -1e30, as those
+    // with a bias below it (-inf among them): finite, so that 0 * (y - m) stays 0.
     float cw = 0.f, cb = 0.f;
-    auto column = [&](int nt, int ch) {
-      const int c = nt * BN + ch * 32 + lane;
+    uint32_t coming = 0;  // residual buffers with a copy in flight
+    auto fetch = [&](int row0, int col0, int buf) {
+      const int c = col0 + lane;
       const bool in = c < a.N;
       cw = in ? __ldg(a.w_scale + c) : 0.f;
       cb = in && a.bias ? __ldg(a.bias + c) : 0.f;
       if constexpr (OUT == kScore) cb = in ? max_nan(cb * kLog2e, kMaskedWord) : kMaskedWord;
+      if constexpr (RES) {
+        if (lane == 0 && col0 < a.N_tma) {
+          bulk_wait_read<1>();  // the store from this buffer, three chunks ago at least, has read it
+          mbar_arrive_expect_tx(res_bar(ew, buf), P::BUF);
+          tma_load_3d(stg + buf * P::BUF, &tmR, res_bar(ew, buf), col0, row0, 0);
+        }
+        if (col0 < a.N_tma) coming |= 1u << buf;
+      }
     };
-    auto row_scale = [&](int mt) {
-      const int row = mt * P::PM + static_cast<int>(rank) * 128 + quarter * 32 + lane;
-      return row < a.rows ? __ldg(a.x_scale + row) * (OUT == kScore ? kLog2e : 1.f) : 0.f;
-    };
-    int acc = 0, it = 0;
-    uint32_t acc_phase = 0;
-    bool ok = true;
+    int acc = 0, buf = 0;
+    uint32_t acc_phase = 0, res_phase = 0;  // res_phase: a bit for each buffer
+    bool ok = true, have = false;           // have: this chunk has been fetched
     TileWalk walk(a, t_first, t_end, t_step);
-    float xs_next = 0.f;
-    if (walk.more()) {
-      column(walk.nt, group);
-      xs_next = row_scale(walk.mt);
-    }
+    float xs_next = walk.more() ? row_scale(walk.mt) : 0.f;
     Stat2 st{kLowest, 0.f, 0.f};
     while (walk.more()) {
       const int mt = walk.mt, nt = walk.nt;
       walk.next();  // the tile after this one
-      const int row0 = mt * P::PM + static_cast<int>(rank) * 128 + quarter * 32;
+      const int row0 = row_of(mt);
       const int row = row0 + lane;
       const bool valid = row < a.rows;
       const float xs = xs_next;
@@ -438,25 +513,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       const uint32_t taddr =
           tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-      for (int ch = group; ch < BN / 32; ch += kGroups) {
+      for (int ch = group; ch < BN / 32; ch += P::GROUPS) {
         const int col0 = nt * BN + ch * 32;
-        if (col0 >= a.N || row0 >= a.rows) {  // warp-uniform; the chunk fetched ahead is another one
-          if (walk.more()) column(walk.nt, group);
-          break;
-        }
+        if (col0 >= a.N || row0 >= a.rows) break;  // warp-uniform
+        if (!have) fetch(row0, col0, buf);
         w_s[lane] = cw;
         b_s[lane] = cb;
         __syncwarp();
-        if (ch + kGroups < BN / 32)
-          column(nt, ch + kGroups);
-        else if (walk.more())
-          column(walk.nt, group);
-        float4 res[RES ? 8 : 1];
-        if constexpr (RES) {
-          const float *rr = a.residual + static_cast<long long>(row) * a.ld_out;
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            res[q] = valid ? load4_rw(rr, col0 + 4 * q, a.N) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const int this_buf = buf;
+        buf = buf + 1 == P::BUFS ? 0 : buf + 1;
+        {
+          // the next chunk: of this tile, or the first of the next one
+          const bool here = ch + P::GROUPS < BN / 32 && col0 + 32 * P::GROUPS < a.N;
+          const int nrow = here ? row0 : row_of(walk.mt);
+          const int ncol = here ? col0 + 32 * P::GROUPS : walk.nt * BN + group * 32;
+          have = (here || walk.more()) && nrow < a.rows && ncol < a.N;
+          if (have) fetch(nrow, ncol, buf);
         }
         float v[32];
         tmem_ld32(taddr + ch * 32, v);
@@ -466,53 +538,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         } else {
           lin_values(v, xs, w_s, b_s, a.relu2);
           __syncwarp();
-          if constexpr (RES) {
+          if (col0 + 32 > a.N_tma && valid) store_rest<OUT, RES>(a, row, col0, v);
+          if (col0 < a.N_tma) {  // warp-uniform
+            const uint32_t at = stg + this_buf * P::BUF;
+            if constexpr (RES) {
+              if (!warp_wait(res_bar(ew, this_buf), res_phase >> this_buf & 1u, abort_flag)) {
+                ok = false;
+                break;
+              }
+              res_phase ^= 1u << this_buf;
+              coming &= ~(1u << this_buf);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              v[4 * q] += res[q].x;
-              v[4 * q + 1] += res[q].y;
-              v[4 * q + 2] += res[q].z;
-              v[4 * q + 3] += res[q].w;
+              for (int c = 0; c < 8; ++c) {
+                float r[4];
+                ld_shared4(at + lin_sw128(lane, c), r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * c + j] += r[j];
+              }
+            } else {
+              // the last store issued from this buffer must have read it
+              if (lane == 0) bulk_wait_read<P::BUFS - 1>();
+              __syncwarp();
             }
-          }
-          if (col0 + 32 > a.N_tma && valid) store_rest<OUT>(a, row, col0, v);
-          if (col0 >= a.N_tma) continue;  // warp-uniform
-          const uint32_t buf = stg + (it % P::BUFS) * P::BUF;
-          if (it >= P::BUFS) {  // the last store issued from this buffer must have read it
-            if (lane == 0) bulk_wait_read<P::BUFS - 1>();
+            if constexpr (OUT == AVEY_F32) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                lin_st4(at + lin_sw128(lane, c), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                        __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+            } else if constexpr (OUT == AVEY_BF16) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                lin_st4(at + lin_sw64(lane, c), pack_bf16(v[8 * c], v[8 * c + 1]),
+                        pack_bf16(v[8 * c + 2], v[8 * c + 3]), pack_bf16(v[8 * c + 4], v[8 * c + 5]),
+                        pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+            } else {
+              uint32_t hi[16], lo[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) split_pack(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                lin_st4(at + lin_sw64(lane, c), hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+                lin_st4(at + 2048 + lin_sw64(lane, c), lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+              }
+            }
+            fence_proxy_async_smem();
             __syncwarp();
-          }
-          if constexpr (OUT == AVEY_F32) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              lin_st4(buf + lin_sw128(lane, c), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                      __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
-          } else if constexpr (OUT == AVEY_BF16) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              lin_st4(buf + lin_sw64(lane, c), pack_bf16(v[8 * c], v[8 * c + 1]),
-                      pack_bf16(v[8 * c + 2], v[8 * c + 3]), pack_bf16(v[8 * c + 4], v[8 * c + 5]),
-                      pack_bf16(v[8 * c + 6], v[8 * c + 7]));
-          } else {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) split_pack(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              lin_st4(buf + lin_sw64(lane, c), hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-              lin_st4(buf + 2048 + lin_sw64(lane, c), lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+            if (lane == 0) {
+              tma_store_3d(&tmO0, at, col0, row0, 0);
+              if constexpr (OUT == AVEY_BF16X2) tma_store_3d(&tmO1, at + 2048, col0, row0, 0);
             }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&tmO0, buf, col0, row0, 0);
-            if constexpr (OUT == AVEY_BF16X2) tma_store_3d(&tmO1, buf + 2048, col0, row0, 0);
-            bulk_commit();
-          }
-          ++it;
+          if (lane == 0) bulk_commit();  // one group a chunk, an empty one too
         }
       }
+      if (!ok) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc ? tempty_r1 : tempty_r0);
@@ -523,7 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         // slot p + mt alone, since both only grow along the tiles
         if (nt == a.tiles_n - 1 || !walk.more()) {
           const long long slot = static_cast<long long>(pair) + mt;
-          a.partial[(slot * kGroups + group) * 256 + static_cast<int>(rank) * 128 + quarter * 32 + lane] =
+          a.partial[(slot * P::GROUPS + group) * 256 + static_cast<int>(rank) * 128 + quarter * 32 + lane] =
               make_float4(st.m, st.s, st.t, 0.f);
           st = Stat2{kLowest, 0.f, 0.f};
         }
@@ -532,6 +611,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     if (!ok) {
       *abort_flag = 1;
       record_status(a.status, AVEY_ERR_DEVICE_TIMEOUT);
+      if constexpr (RES) {
+        // residual copies in flight must land before the block leaves
+        if (lane == 0)
+          for (int i = 0; i < P::BUFS; ++i)
+            if (coming >> i & 1u) drain_wait(res_bar(ew, i), res_phase >> i & 1u);
+      }
     }
     if (OUT != kScore && lane == 0) bulk_wait_all();  // outputs written
   }
@@ -548,19 +633,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   cluster_sync_all();
 }
 
-template <int BN, int OUT, bool RES>
+template <int BN, int OUT, bool RES, bool ARES>
 avey_status run_linear_pair(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &o0,
-                            const CUtensorMap &o1, const LinArgs &a, int pairs, cudaStream_t st) {
-  using P = LinLayout<BN, OUT>;
-  auto kern = linear_i8_pair<BN, OUT, RES>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(P::SMEM_BYTES));
+                            const CUtensorMap &o1, const CUtensorMap &r, LinArgs a, int pairs, cudaStream_t st) {
+  using P = LinLayout<BN, OUT, RES, ARES>;
+  auto kern = linear_i8_pair<BN, OUT, RES, ARES>;
+  const int ksteps = (a.K + kBK - 1) / kBK;
+  a.stages = P::stages(ksteps);
+  a.tiles_bytes = P::tiles_bytes(ksteps);
+  const uint32_t bytes = a.tiles_bytes + P::REST_BYTES;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
   if (e != cudaSuccess) {
     cudaGetLastError();
     set_detail("linear_i8: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     return AVEY_ERR_CUDA;
   }
-  kern<<<2 * pairs, kLinThreads, P::SMEM_BYTES, st>>>(ma, mb, o0, o1, a);
+  kern<<<2 * pairs, P::THREADS, bytes, st>>>(ma, mb, o0, o1, r, a);
   AVEY_CHECK_LAUNCH(OUT == kScore ? "score_i8" : "linear_i8", st);
   return AVEY_OK;
 }
@@ -590,11 +678,23 @@ avey_status run_linear_bn(const avey_linear_i8_params *p, const int8_t *xq, int6
       !encode_map(&o1, false, static_cast<bf16 *>(out) + static_cast<long long>(a.rows) * a.ld_out, inner,
                   a.rows, 1, rs, rs * a.rows, 32, 32, 64))
     return AVEY_ERR_CUDA;
+  CUtensorMap mr = o0;
+  if (a.residual && !encode_map(&mr, true, a.residual, inner, a.rows, 1, rs, rs * a.rows, 32, 32, 128))
+    return AVEY_ERR_CUDA;
   const int pairs = pairs_for(a.num_tiles);
-  if (out_dt == AVEY_BF16) return run_linear_pair<BN, AVEY_BF16, false>(ma, mb, o0, o1, a, pairs, s);
-  if (out_dt == AVEY_BF16X2) return run_linear_pair<BN, AVEY_BF16X2, false>(ma, mb, o0, o1, a, pairs, s);
-  if (a.residual) return run_linear_pair<BN, AVEY_F32, true>(ma, mb, o0, o1, a, pairs, s);
-  return run_linear_pair<BN, AVEY_F32, false>(ma, mb, o0, o1, a, pairs, s);
+#define AVEY_LINEAR(OUT, ARES) run_linear_pair<BN, OUT, false, ARES>(ma, mb, o0, o1, mr, a, pairs, s)
+  if (a.residual) return run_linear_pair<BN, AVEY_F32, true, false>(ma, mb, o0, o1, mr, a, pairs, s);
+  if constexpr (BN == 256) {
+    if (a.K <= kBK * kResidentSteps) {
+      if (out_dt == AVEY_BF16) return AVEY_LINEAR(AVEY_BF16, true);
+      if (out_dt == AVEY_BF16X2) return AVEY_LINEAR(AVEY_BF16X2, true);
+      return AVEY_LINEAR(AVEY_F32, true);
+    }
+  }
+  if (out_dt == AVEY_BF16) return AVEY_LINEAR(AVEY_BF16, false);
+  if (out_dt == AVEY_BF16X2) return AVEY_LINEAR(AVEY_BF16X2, false);
+  return AVEY_LINEAR(AVEY_F32, false);
+#undef AVEY_LINEAR
 }
 
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
@@ -722,6 +822,8 @@ extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void
 namespace avey {
 namespace {
 
+constexpr int kScoreGroups = LinLayout<256, kScore, false, true>::GROUPS;
+
 // One warp per row: joins the row's partial statistics, and computes the given
 // token's logit again from its K bytes of either operand.
 __global__ void __launch_bounds__(256)
@@ -734,14 +836,15 @@ __global__ void __launch_bounds__(256)
   const long long first = static_cast<long long>(mt) * a.tiles_n, last = first + a.tiles_n - 1;
   // the pairs whose shares hold tiles first .. last
   long long p0 = first * npairs / a.num_tiles, p1 = last * npairs / a.num_tiles;
-  while (score_start(p0 + 1, a.num_tiles, npairs) <= first) ++p0;
-  while (score_start(p0, a.num_tiles, npairs) > first) --p0;
-  while (score_start(p1 + 1, a.num_tiles, npairs) <= last) ++p1;
-  while (score_start(p1, a.num_tiles, npairs) > last) --p1;
+  while (share_start(p0 + 1, a.num_tiles, npairs) <= first) ++p0;
+  while (share_start(p0, a.num_tiles, npairs) > first) --p0;
+  while (share_start(p1 + 1, a.num_tiles, npairs) <= last) ++p1;
+  while (share_start(p1, a.num_tiles, npairs) > last) --p1;
   Stat2 st{kLowest, 0.f, 0.f};
-  const int parts = kGroups * static_cast<int>(p1 - p0 + 1);
+  constexpr int G = kScoreGroups;
+  const int parts = G * static_cast<int>(p1 - p0 + 1);
   for (int i = lane; i < parts; i += 32) {
-    const float4 v = a.partial[((p0 + i / kGroups + mt) * kGroups + i % kGroups) * 256 + (row & 255)];
+    const float4 v = a.partial[((p0 + i / G + mt) * G + i % G) * 256 + (row & 255)];
     Stat2 o{v.x, v.y, v.z};
     const float M = fmaxf(st.m, o.m);
     rebase2(st, M);
@@ -796,7 +899,7 @@ constexpr int kFewRows = 32;
 inline int64_t score_ld(int N) { return (static_cast<int64_t>(N) + 7) / 8 * 8; }
 inline size_t score_partial_bytes(int rows) {
   const size_t slots = static_cast<size_t>((rows + 255) / 256) + std::max(1, sm_count() / 2);
-  return slots * kGroups * 256 * sizeof(float4);
+  return slots * kScoreGroups * 256 * sizeof(float4);
 }
 
 avey_status launch_score_i8(const avey_linear_i8_params *p, const int8_t *xq, int64_t ld_xq,
@@ -818,7 +921,9 @@ avey_status launch_score_i8(const avey_linear_i8_params *p, const int8_t *xq, in
   CUtensorMap ma, mb;
   if (!encode_i8_map(&ma, xq, a.K, rows, ld_xq, 128)) return AVEY_ERR_CUDA;
   if (!encode_i8_map(&mb, p->Wq, a.K, a.N, p->ld_w, 128)) return AVEY_ERR_CUDA;
-  const avey_status st = run_linear_pair<256, kScore, false>(ma, mb, ma, ma, a, pairs, s);
+  const avey_status st = a.K <= kBK * kResidentSteps
+                             ? run_linear_pair<256, kScore, false, true>(ma, mb, ma, ma, ma, a, pairs, s)
+                             : run_linear_pair<256, kScore, false, false>(ma, mb, ma, ma, ma, a, pairs, s);
   if (st != AVEY_OK) return st;
   score_join<<<(rows + 7) / 8, 256, 0, s>>>(a, pairs, xq, ld_xq, p->Wq, p->ld_w, ids, logprob, stats, entropy);
   AVEY_CHECK_LAUNCH("score_join", s);
