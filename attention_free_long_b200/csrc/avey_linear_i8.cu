@@ -480,10 +480,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
     uint32_t coming = 0;  // residual buffers with a copy in flight
     auto fetch = [&](int row0, int col0, int buf) {
       const int c = col0 + lane;
-      const bool in = c < a.N;
-      cw = in ? __ldg(a.w_scale + c) : 0.f;
-      cb = in && a.bias ? __ldg(a.bias + c) : 0.f;
-      if constexpr (OUT == kScore) cb = in ? max_nan(cb * kLog2e, kMaskedWord) : kMaskedWord;
+      cw = 0.f;
+      cb = OUT == kScore ? kMaskedWord : 0.f;
+      if (c < a.N) {  // nothing is computed from the loads before they are stored
+        cw = __ldg(a.w_scale + c);
+        if (a.bias)
+          cb = __ldg(a.bias + c);
+        else if (OUT == kScore)
+          cb = 0.f;
+      }
       if constexpr (RES) {
         if (lane == 0 && col0 < a.N_tma) {
           bulk_wait_read<1>();  // the store from this buffer, three chunks ago at least, has read it
@@ -520,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
         if (col0 >= a.N || row0 >= a.rows) break;  // warp-uniform
         if (!have) fetch(row0, col0, buf);
         w_s[lane] = cw;
-        b_s[lane] = cb;
+        b_s[lane] = OUT == kScore ? max_nan(cb * kLog2e, kMaskedWord) : cb;
         __syncwarp();
         const int this_buf = buf;
         buf = buf + 1 == P::BUFS ? 0 : buf + 1;
