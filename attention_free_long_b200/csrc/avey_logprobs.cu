@@ -10,9 +10,10 @@
 // few rows, whose partial results meet in distributed shared memory.
 // Alternatives: the `top`-th largest of the threads' maxima is a bar that `top`
 // elements reach, so every alternative reaches it and lies with a thread whose
-// maximum does: about `top` of them.  Their vectors (top / 256 of the row) are
-// read a second time, and what reaches the bar goes through sorted lists, one a
-// warp.  The streaming loop carries nothing for this.
+// maximum does: about `top` of them.  A thread knows which batch its maximum
+// came from and the largest maximum of its other batches; mostly that one is
+// below the bar, and eight vectors of the thread are read a second time, four
+// threads' at once.  What reaches the bar goes through sorted lists, one a warp.
 // Backward: dx_j = g (1[j = id] - p_j) - h p_j (log p_j + entropy), one read and
 // one write of the row.
 #include <algorithm>
@@ -25,7 +26,7 @@ namespace avey {
 namespace {
 
 constexpr int kLpThreads = 256;       // threads of the gradient's blocks
-constexpr int kBatch = 4;             // 16-byte vectors a thread takes at once
+constexpr int kBatch = 8;             // 16-byte vectors a thread takes at once
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
 // exp(d) is 0 in fp32 from here down; keeps 0 * (x - m) finite
@@ -77,13 +78,16 @@ struct Vec<float> {
   static __device__ __forceinline__ float max(const uint4 &w) {
     return fmaxf(max3f(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z)), __uint_as_float(w.w));
   }
-  static __device__ __forceinline__ float max4(const uint4 *w) {
-    return fmaxf(max3f(max(w[0]), max(w[1]), max(w[2])), max(w[3]));
+  static __device__ __forceinline__ float max_all(const uint4 *w) {
+    float m = max(w[0]);
+#pragma unroll
+    for (int i = 1; i < kBatch; ++i) m = fmaxf(m, max(w[i]));
+    return m;
   }
-  static __device__ __forceinline__ float min4(const uint4 *w) {
+  static __device__ __forceinline__ float min_all(const uint4 *w) {
     float m = INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kBatch; ++i)
       m = min3f(min3f(m, __uint_as_float(w[i].x), __uint_as_float(w[i].y)), __uint_as_float(w[i].z),
                 __uint_as_float(w[i].w));
     return m;
@@ -115,17 +119,17 @@ struct Vec<bf16> {
     const __nv_bfloat162 m = __hmax2(__hmax2(b2(w.x), b2(w.y)), __hmax2(b2(w.z), b2(w.w)));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  static __device__ __forceinline__ float max4(const uint4 *w) {
+  static __device__ __forceinline__ float max_all(const uint4 *w) {
     __nv_bfloat162 m = b2(w[0].x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kBatch; ++i)
       m = __hmax2(__hmax2(__hmax2(m, b2(w[i].x)), b2(w[i].y)), __hmax2(b2(w[i].z), b2(w[i].w)));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  static __device__ __forceinline__ float min4(const uint4 *w) {
+  static __device__ __forceinline__ float min_all(const uint4 *w) {
     __nv_bfloat162 m = b2(w[0].x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kBatch; ++i)
       m = __hmin2(__hmin2(__hmin2(m, b2(w[i].x)), b2(w[i].y)), __hmin2(b2(w[i].z), b2(w[i].w)));
     return fminf(__low2float(m), __high2float(m));
   }
@@ -198,10 +202,23 @@ __device__ __forceinline__ void add_terms(const uint4 &w, float m, float2 &s, fl
   }
 }
 
-// A batch of vectors into a thread's statistics; s and t are the running sums.
-template <typename T>
-__device__ __forceinline__ void add_batch(const uint4 (&w)[kBatch], Stat &st, float2 &s, float2 &t) {
-  const float top = Vec<T>::max4(w);
+// With TOP: a thread's largest value, the first vector of the batch it came from,
+// and the largest value of the other batches.
+struct Best {
+  float first = -INFINITY, second = -INFINITY;
+  int batch = 0;
+};
+
+// A batch of vectors u, u + stride, .. into a thread's statistics; s and t are
+// the running sums.
+template <typename T, bool TOP>
+__device__ __forceinline__ void add_batch(const uint4 (&w)[kBatch], int u, Stat &st, float2 &s, float2 &t, Best &best) {
+  const float top = Vec<T>::max_all(w);
+  if constexpr (TOP) {
+    best.second = fmaxf(best.second, fminf(best.first, top));
+    best.batch = top > best.first ? u : best.batch;
+    best.first = fmaxf(best.first, top);
+  }
   if (top > st.m) {
     st.s = s.x + s.y;
     st.t = t.x + t.y;
@@ -209,7 +226,7 @@ __device__ __forceinline__ void add_batch(const uint4 (&w)[kBatch], Stat &st, fl
     s = make_float2(st.s, 0.f);
     t = make_float2(st.t, 0.f);
   }
-  if (Vec<T>::min4(w) >= kLow) {
+  if (Vec<T>::min_all(w) >= kLow) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) add_terms<T, false>(w[i], st.m, s, t);
   } else {
@@ -390,33 +407,40 @@ __device__ __forceinline__ void insert_top(const uint4 &w, bool in, uint32_t e0,
   }
 }
 
-// The elements of at least `bar` of this warp's threads (those whose maximum
-// `best` reaches it), as one descending list of 32 over the lanes.  first: the
-// first vector of lane 0.  Four threads' vectors are on their way at once.
+// The elements of at least `bar` of this warp's threads, as one descending list
+// of 32 over the lanes.  first: the first vector of lane 0.
 template <typename T>
-__device__ __forceinline__ uint64_t select_top(const Row<T> &r, int first, int stride, float best, float bar, int lane) {
+__device__ __forceinline__ uint64_t select_top(const Row<T> &r, int first, int stride, const Best &best, float bar, int lane) {
+  static_assert(kBatch == 8, "a batch of four threads to a warp");
   uint64_t list = 0;
-  uint32_t owners = __ballot_sync(0xffffffffu, best >= bar && best > -INFINITY);
-  while (owners) {
-    int owner[4];
+  const bool mine = best.first >= bar && best.first > -INFINITY;
+  uint32_t all = __ballot_sync(0xffffffffu, mine && best.second >= bar);
+  uint32_t one = __ballot_sync(0xffffffffu, mine) & ~all;
+  // threads of which one batch reaches the bar, four at a time
+  while (one) {
+    int owner = 32;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      owner[i] = owners ? __ffs(owners) - 1 : 32;
-      owners &= owners - 1;
+      if (lane >> 3 == i && one) owner = __ffs(one) - 1;
+      one &= one - 1;
     }
-    // offset of this lane's vector of the first thread; the others' are beside it
-    for (long long u0 = first + static_cast<long long>(lane) * stride; __any_sync(0xffffffffu, u0 < r.vecs);
-         u0 += 32ll * stride) {
-      uint4 w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (owner[i] < 32 && u0 + owner[i] < r.vecs) w[i] = r.load(static_cast<int>(u0) + owner[i]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (owner[i] == 32) break;
-        insert_top<T>(w[i], u0 + owner[i] < r.vecs, static_cast<uint32_t>(r.first(static_cast<int>(u0) + owner[i])),
-                      bar, list, lane);
-      }
+    const int batch = __shfl_sync(0xffffffffu, best.batch, owner & 31);
+    const long long u = batch + static_cast<long long>(lane & 7) * stride;
+    const bool in = owner < 32 && u < r.vecs;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (in) w = r.load(static_cast<int>(u));
+    insert_top<T>(w, in, static_cast<uint32_t>(r.first(static_cast<int>(u))), bar, list, lane);
+  }
+  // threads of which several do
+  while (all) {
+    const int owner = first + __ffs(all) - 1;
+    all &= all - 1;
+    for (long long u0 = owner; u0 < r.vecs; u0 += 32ll * stride) {
+      const long long u = u0 + static_cast<long long>(lane) * stride;
+      const bool in = u < r.vecs;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (in) w = r.load(static_cast<int>(u));
+      insert_top<T>(w, in, static_cast<uint32_t>(r.first(static_cast<int>(u))), bar, list, lane);
     }
   }
   return list;
@@ -461,6 +485,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? 8 : 32 / W) to
   int id = writer && a.ids ? a.ids[row] : -1;
 
   Stat st{kLowest, 0.f, 0.f};
+  Best best;
   {
     float2 s2 = make_float2(0.f, 0.f), t2 = s2;
     const int whole_end = static_cast<int>((static_cast<long long>(a.V) + r.shift) / N);
@@ -471,7 +496,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? 8 : 32 / W) to
         uint4 w[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) w[i] = __ldg(src + u + i * stride);
-        add_batch<T>(w, st, s2, t2);
+        add_batch<T, TOP>(w, u, st, s2, t2, best);
       }
     }
     for (; u < r.vecs; u += kBatch * stride) {
@@ -481,16 +506,15 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? 8 : 32 / W) to
         w[i] = make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf);
         if (u + i * stride < r.vecs) w[i] = r.load(u + i * stride);
       }
-      add_batch<T>(w, st, s2, t2);
+      add_batch<T, TOP>(w, u, st, s2, t2, best);
     }
     st.s = s2.x + s2.y;
     st.t = t2.x + t2.y;
   }
   const float x_id = writer ? given_logit(a, r, id) : 0.f;  // not needed before the sums are joined
-  const float best = st.s > 0.f ? st.m : -INFINITY;          // this thread's maximum
   uint32_t sorted = 0;
   if constexpr (TOP) {
-    sorted = warp_sort(ord_of(best), lane);
+    sorted = warp_sort(ord_of(best.first), lane);
     if (W > 1) maxima[warp][lane] = sorted;
   }
   Stat all = row_stats<W>(st, sm, warp, lane);
@@ -577,7 +601,7 @@ avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
   // Few rows: several blocks a row, as long as a thread has four vectors and the
   // blocks find room at once (1 x 50368 fp32: 9.8 us with one, 6.8 with eight;
   // 300 rows: 14.8 with one, 20.6 with two).  Many rows: fewer warps to a row,
-  // whose ends cost less (6554 x 50368 bf16: 120 us with eight, 112 with four;
+  // whose ends cost less (6554 x 50368 bf16: 115 us with eight, 107 with four;
   // 2000 x 2000: 10.4 with eight, 5.9 with four, 4.8 with one), unless a long
   // row would be left to one warp at the end.
   while (a.blocks < 8 && static_cast<long long>(rows) * a.blocks * 2 <= 2ll * sms && vecs >= 1024ll * a.blocks)
