@@ -122,9 +122,10 @@ avey_status check_linear_i8(const char *fn, const avey_linear_i8_params *p, cons
 avey_status launch_linear_i8(const avey_linear_i8_params *p, const int8_t *xq, int64_t ld_xq,
                              const float *x_scale, int rows, const float *residual, void *out,
                              avey_dtype out_dt, int64_t ld_out, cudaStream_t s);
-// The same for up to 32 rows (avey_linear_few.cu): whether the kernel takes this
-// many rows of K values, whether it also quantises them, and the product.  x of
-// type AVEY_I8 comes with x_scale, other types without.
+// The same for few rows (avey_linear_few.cu): whether the kernel takes this many
+// rows of K values, whether it also quantises them, and the product.  x of type
+// AVEY_I8 comes with x_scale, other types without.
+constexpr int kFewRows = 16;
 bool linear_few_fits(int rows, int K);
 bool linear_few_quantizes(avey_dtype x_dt, int rows, int K);
 avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt, int64_t ld_x,

@@ -1,4 +1,4 @@
-// avey_linear_few.cu -- the 8-bit product for up to 32 rows (single tokens of a
+// avey_linear_few.cu -- the 8-bit product for up to 16 rows (single tokens of a
 // decoder or a head): bound by one read of the weights, and by latency.
 //
 // A warp owns 16 output channels and walks K in steps of 64: mma.sync m16n8k32
@@ -8,10 +8,11 @@
 // k = 16 q .. 16 q + 15 of its channels (g and g + 8) and of token g, and two
 // MMAs eat them as "columns" 4 q .. and 16 + 4 q ..  A warp's loads cover whole
 // 64-byte pieces of 16 rows; rows are prefetched into L2 before the block
-// prepares its tokens.  Up to 16 rows are quantised by every block for itself
-// (a few KB from L2), which saves the launch of the rounding kernel.
-// 128-row tiles of tcgen05 would spend the same reads on rows that are not
-// there: one token against 50368 x 768 weights took 22 us that way.
+// prepares its tokens.  Rows that come unrounded are quantised by every block for
+// itself (a few KB from L2), which saves the launch of the rounding kernel.
+// 16 rows of 8-bit integers against 50368 x 768 weights take 10.1 us here and
+// 16.1 us as a tile of 256; from 17 rows on the tile wins (20 rows against
+// 1536 x 768: 9.8 and 6.3 us), since more rows mean more to prepare per block.
 #include <algorithm>
 
 #include "avey_common.cuh"
@@ -227,16 +228,16 @@ avey_status run_few_out(const FewArgs &a, avey_dtype out_dt, cudaStream_t s) {
 constexpr int kFewShared = 96 * 1024;  // at most two blocks' worth of an SM
 
 inline int few_stride(int K) { return (K + 127) / 128 * 128 + 64; }  // odd multiples of 64: no bank conflicts
-inline int few_blocks(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+inline int few_blocks(int rows) { return rows <= 8 ? 1 : 2; }
 
 }  // namespace
 
 bool linear_few_fits(int rows, int K) {
-  return rows <= 32 && static_cast<long long>(few_blocks(rows)) * 8 * few_stride(K) <= kFewShared;
+  return rows <= kFewRows && static_cast<long long>(few_blocks(rows)) * 8 * few_stride(K) <= kFewShared;
 }
 
 bool linear_few_quantizes(avey_dtype x_dt, int rows, int K) {
-  return x_dt != AVEY_I8 && rows <= 16 && linear_few_fits(rows, K);
+  return x_dt != AVEY_I8 && linear_few_fits(rows, K);
 }
 
 avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt, int64_t ld_x,
@@ -260,16 +261,13 @@ avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, ave
   a.relu2 = p->act == AVEY_ACT_RELU2;
   a.out = out;
   a.ld_out = ld_out;
-  const int nb = few_blocks(rows);
-#define AVEY_FEW(DT)                                        \
-  return nb == 1 ? run_few_out<1, DT>(a, out_dt, s) : run_few_out<2, DT>(a, out_dt, s)
+  const bool one = few_blocks(rows) == 1;
+#define AVEY_FEW(DT) return one ? run_few_out<1, DT>(a, out_dt, s) : run_few_out<2, DT>(a, out_dt, s)
   switch (x_dt) {
     case AVEY_F32: AVEY_FEW(AVEY_F32);
     case AVEY_BF16: AVEY_FEW(AVEY_BF16);
     case AVEY_BF16X2: AVEY_FEW(AVEY_BF16X2);
-    default:
-      if (nb == 4) return run_few_out<4, AVEY_I8>(a, out_dt, s);
-      AVEY_FEW(AVEY_I8);
+    default: AVEY_FEW(AVEY_I8);
   }
 #undef AVEY_FEW
 }

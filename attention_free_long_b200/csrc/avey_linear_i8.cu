@@ -7,10 +7,13 @@
 // tile overlaps the MMAs of the next.  A K step is 128 bytes = 128 values, four
 // MMAs of K = 32.
 //
-// What bounds it: an SM takes about 41 bytes a cycle from L2, and a 256 x 256
-// tile needs 64 (32 KB a K step of 512 cycles): 8192^3 runs at 3.0 POP/s.  Up to
-// K = 1024 a pair therefore keeps its 256 rows of x in shared memory and walks
-// the channels (ARES), which halves that; then the epilogue bounds.
+// What bounds it: long contractions the tensor pipe (8192^3 to bf16 runs at 3.0
+// POP/s, 0.97 of what the pipe does at the 1.33 GHz that the power cap leaves it);
+// short ones the epilogue, which has 3072 tensor cycles a tile of K = 768 to get
+// 32768 sums out of TMEM and takes about 5000.  Up to K = 1024 a pair keeps its
+// 256 rows of x in shared memory and walks the channels (ARES): half the bytes
+// from L2 and into shared memory, 44 instead of 48 us for 8192 x 768 x 8192 to
+// bf16.
 #include <algorithm>
 
 #include "avey_common.cuh"
@@ -724,10 +727,13 @@ avey_status launch_linear_i8(const avey_linear_i8_params *p, const int8_t *xq, i
   a.residual = residual;
   a.ld_out = ld_out;
   a.status = device_status_word();
-  // the widest tile that still gives every pair of SMs one
+  // The widest tile that gives every pair of SMs one, 128 columns down to every
+  // second pair (1003 x 1008 x 2048: 9.8 us with 64, 9.0 with 128, 11.2 with 256;
+  // 256 x 256 x 256: 5.5, 6.4 and 8.2; 4096 x 768 x 1536: 16.4, 12.2 and 12.4;
+  // 32768 x 768 x 1536: 64, 44 and 38).
   const long long tm = (rows + 255) / 256, pairs = sm_count() / 2;
   if (tm * ((p->N + 255) / 256) >= pairs) return run_linear_bn<256>(p, xq, ld_xq, a, out, out_dt, s);
-  if (tm * ((p->N + 127) / 128) >= pairs) return run_linear_bn<128>(p, xq, ld_xq, a, out, out_dt, s);
+  if (2 * tm * ((p->N + 127) / 128) >= pairs) return run_linear_bn<128>(p, xq, ld_xq, a, out, out_dt, s);
   return run_linear_bn<64>(p, xq, ld_xq, a, out, out_dt, s);
 }
 
@@ -897,9 +903,6 @@ __global__ void __launch_bounds__(256)
         bad ? make_float2(nan, nan) : empty ? make_float2(-INFINITY, 0.f) : make_float2(st.m * kLn2, z);
   if (entropy) entropy[row] = bad ? nan : empty ? 0.f : fmaf(-kLn2, st.t / st.s, z);
 }
-
-// Up to this many rows the logits go through the workspace, row by row.
-constexpr int kFewRows = 32;
 
 inline int64_t score_ld(int N) { return (static_cast<int64_t>(N) + 7) / 8 * 8; }
 inline size_t score_partial_bytes(int rows) {

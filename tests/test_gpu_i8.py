@@ -138,7 +138,8 @@ def _weights(N, K, seed, dev, bias):
 def _product(x, q, w, b, act, res):
     """(y, bound of the fp32 kernel's error) in float64."""
     xq, s = _ref_rows(x)
-    p = (xq @ q.T).astype(np.float64) * s.astype(np.float64)[:, None] * w.astype(np.float64)[None]
+    # float64 products of whole numbers are exact here
+    p = (xq.astype(np.float64) @ q.T.astype(np.float64)) * s.astype(np.float64)[:, None] * w.astype(np.float64)[None]
     y = p + (0 if b is None else b.astype(np.float64))
     err = 2 * U * np.abs(p) + U * np.abs(y)
     if act:
@@ -154,9 +155,11 @@ def _product(x, q, w, b, act, res):
 SHAPES = [(1, 768, 1000), (1, 5, 1), (2, 16, 7), (7, 31, 64), (8, 768, 257), (9, 127, 65), (16, 128, 8),
           (33, 129, 255), (64, 768, 1536), (129, 1000, 96), (257, 100, 300), (300, 2048, 33), (1025, 64, 513), (24, 500, 77),
           (30, 5000, 40), (12, 7000, 9700), (17, 64, 1), (32, 1025, 130)]
+# tiles of 128 and of 256 columns, x resident or not, several row blocks to a pair of SMs
+WIDE = [(700, 100, 4000), (2000, 300, 9001), (1500, 1100, 4004), (40000, 64, 300)]
 
 
-@pytest.mark.parametrize("rows,K,N", SHAPES)
+@pytest.mark.parametrize("rows,K,N", SHAPES + WIDE)
 @pytest.mark.parametrize("kind,out", [("f32", "f32"), ("bf16", "bf16"), ("pair", "pair"), ("strided", "f32")])
 def test_product(rows, K, N, kind, out, cuda_dev):
     act, bias = (rows + N) % 2, K % 2 == 0
@@ -177,7 +180,8 @@ def test_product(rows, K, N, kind, out, cuda_dev):
     assert (np.abs(got.double().cpu().numpy() - y) <= err).all()
 
 
-@pytest.mark.parametrize("rows,K,N", [(1, 64, 40), (5, 100, 13), (70, 768, 200), (300, 1536, 768)])
+@pytest.mark.parametrize("rows,K,N", [(1, 64, 40), (5, 100, 13), (70, 768, 200), (300, 1536, 768),
+                                      (600, 40, 4001), (3001, 100, 2050)])
 def test_residual_alone_and_in_place(rows, K, N, cuda_dev):
     lin, q, w, b = _weights(N, K, 5, cuda_dev, True)
     x = _activations(rows, K, 6)

@@ -83,10 +83,9 @@ def test_one_layer_stays_near_the_16_bit_one(cuda_dev):
     assert (np.abs(D(got) - D(want)) <= bound).all()
 
 
-@pytest.mark.parametrize("rows", [1, 9, 700])
-@pytest.mark.parametrize("V", [1, 1000, 5003])
-def test_score_is_product_then_scores(rows, V, cuda_dev):
-    d = 136
+@pytest.mark.parametrize("rows,V,d", [(r, V, 136) for r in (1, 9, 17, 700) for V in (1, 1000, 5003)]
+                         + [(300, 3001, 1040), (2600, 700, 64), (40, 70000, 72)])
+def test_score_is_product_then_scores(rows, V, d, cuda_dev):
     head = _head(V, d, cuda_dev)
     g = torch.Generator(device=cuda_dev).manual_seed(rows)
     h = torch.randn(rows, d, device=cuda_dev, generator=g) * 4
@@ -171,7 +170,7 @@ def test_encoder_to_fill_mask_and_loss(cuda_dev):
     ref = logits.double().requires_grad_()
     loss = torch.nn.functional.cross_entropy(ref, ids.long())
     loss.backward()
-    assert abs(float(-full.logprob.mean()) - float(loss)) <= 1e-5 * float(loss)
+    assert abs(float(-full.logprob.mean()) - loss.item()) <= 1e-5 * loss.item()
     torch.testing.assert_close(dx.double(), ref.grad, rtol=1e-4, atol=1e-9)
     torch.cuda.synchronize()
     assert av.device_status() == 0
