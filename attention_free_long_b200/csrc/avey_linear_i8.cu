@@ -70,7 +70,9 @@ struct LinLayout {
   static constexpr int BUFS = RES ? 3 : 1;
   static constexpr uint32_t STAGING_BYTES = EPI * BUFS * BUF;
   static constexpr uint32_t CTRL_BYTES = 1024;
-  static constexpr uint32_t COLS_BYTES = EPI * 2 * 32 * 4;  // each warp's scale and bias
+  // each warp's scales and biases: of a chunk, for the scores of all its chunks of a tile
+  static constexpr int CHUNKS = OUT == kScore ? BN / 32 / GROUPS : 1;
+  static constexpr uint32_t COLS_BYTES = EPI * CHUNKS * 64 * 4;
   static constexpr uint32_t REST_BYTES = STAGING_BYTES + CTRL_BYTES + COLS_BYTES + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
   // stages and shared memory for this many K steps
@@ -241,16 +243,18 @@ __device__ __forceinline__ void score_values(float (&v)[32], float xs, const flo
   }
   rebase2(st, fmaxf(st.m, max32(v)));
   const float2 minus = make_float2(-st.m, -st.m);
-  float2 s = make_float2(0.f, 0.f), t = s;
+  float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, t[2] = {s[0], s[0]};
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    float2 d = fadd2(make_float2(v[2 * j], v[2 * j + 1]), minus);
+    const float2 d = fadd2(make_float2(v[2 * j], v[2 * j + 1]), minus);
     const float2 e = make_float2(ex2(d.x), ex2(d.y));
-    s = fadd2(s, e);
-    t = ffma2(e, d, t);
+    s[j & 1] = fadd2(s[j & 1], e);
+    t[j & 1] = ffma2(e, d, t[j & 1]);
   }
-  st.s += s.x + s.y;
-  st.t += t.x + t.y;
+  s[0] = fadd2(s[0], s[1]);
+  t[0] = fadd2(t[0], t[1]);
+  st.s += s[0].x + s[0].y;
+  st.t += t[0].x + t[0].y;
 }
 
 template <int BN, int OUT, bool RES, bool ARES>
@@ -469,43 +473,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
     const int ew = warp - 2, quarter = warp & 3, group = ew >> 2;
     const uint32_t stg = gbase + static_cast<uint32_t>(ew) * P::BUFS * P::BUF;
     const uint32_t tempty_r0 = mapa_shared(tempty_bar(0), 0), tempty_r1 = mapa_shared(tempty_bar(1), 0);
-    float *w_s = reinterpret_cast<float *>(ctrl + P::CTRL_BYTES) + ew * 64, *b_s = w_s + 32;
+    float *cols = reinterpret_cast<float *>(ctrl + P::CTRL_BYTES) + ew * P::CHUNKS * 64;  // [chunk][scale, bias][32]
     auto row_of = [&](int mt) { return mt * P::PM + static_cast<int>(rank) * 128 + quarter * 32; };
     auto row_scale = [&](int mt) {
       const int row = row_of(mt) + lane;
       return row < a.rows ? __ldg(a.x_scale + row) * (OUT == kScore ? kLog2e : 1.f) : 0.f;
     };
-    // Fetches, a chunk ahead, scale and bias of this lane's column of a chunk,
-    // and the chunk's residual into staging buffer `buf`.  The scores work in
-    // units of log 2, where words past the last have the value -1e30, as those
-    // with a bias below it (-inf among them): finite, so that 0 * (y - m) stays 0.
-    float cw = 0.f, cb = 0.f;
-    uint32_t coming = 0;  // residual buffers with a copy in flight
-    auto fetch = [&](int row0, int col0, int buf) {
-      const int c = col0 + lane;
-      cw = 0.f;
-      cb = OUT == kScore ? kMaskedWord : 0.f;
-      if (c < a.N) {  // nothing is computed from the loads before they are stored
-        cw = __ldg(a.w_scale + c);
-        if (a.bias)
-          cb = __ldg(a.bias + c);
-        else if (OUT == kScore)
-          cb = 0.f;
-      }
-      if constexpr (RES) {
-        if (lane == 0 && col0 < a.N_tma) {
-          bulk_wait_read<1>();  // the store from this buffer, three chunks ago at least, has read it
-          mbar_arrive_expect_tx(res_bar(ew, buf), P::BUF);
-          tma_load_3d(stg + buf * P::BUF, &tmR, res_bar(ew, buf), col0, row0, 0);
+    // Scale and bias of this lane's column of CHUNKS chunks from column block nt,
+    // chunk ch: fetched a chunk (scores: a tile) ahead, and nothing is computed
+    // from the loads before they are stored.  The scores work in units of log 2,
+    // where words past the last have the value -1e30, as those with a bias below
+    // it (-inf among them): finite, so that 0 * (y - m) stays 0.
+    float cw[P::CHUNKS], cb[P::CHUNKS];
+    auto fetch_columns = [&](int nt, int ch) {
+#pragma unroll
+      for (int i = 0; i < P::CHUNKS; ++i) {
+        const int c = nt * BN + (ch + i * P::GROUPS) * 32 + lane;
+        cw[i] = 0.f;
+        cb[i] = OUT == kScore ? kMaskedWord : 0.f;
+        if (c < a.N) {
+          cw[i] = __ldg(a.w_scale + c);
+          if (a.bias)
+            cb[i] = __ldg(a.bias + c);
+          else if (OUT == kScore)
+            cb[i] = 0.f;
         }
-        if (col0 < a.N_tma) coming |= 1u << buf;
       }
+    };
+    auto put_columns = [&]() {
+#pragma unroll
+      for (int i = 0; i < P::CHUNKS; ++i) {
+        cols[i * 64 + lane] = cw[i];
+        cols[i * 64 + 32 + lane] = OUT == kScore ? max_nan(cb[i] * kLog2e, kMaskedWord) : cb[i];
+      }
+      __syncwarp();
+    };
+    // The residual of a chunk into staging buffer `to`, a chunk ahead.
+    uint32_t coming = 0;  // buffers with a copy in flight
+    auto fetch_residual = [&](int row0, int col0, int to) {
+      if (col0 >= a.N_tma) return;
+      if (lane == 0) {
+        bulk_wait_read<1>();  // the store from this buffer, three chunks ago at least, has read it
+        mbar_arrive_expect_tx(res_bar(ew, to), P::BUF);
+        tma_load_3d(stg + to * P::BUF, &tmR, res_bar(ew, to), col0, row0, 0);
+      }
+      coming |= 1u << to;
     };
     int acc = 0, buf = 0;
     uint32_t acc_phase = 0, res_phase = 0;  // res_phase: a bit for each buffer
-    bool ok = true, have = false;           // have: this chunk has been fetched
+    bool ok = true, have = false;           // have: this chunk's columns and residual have been fetched
     TileWalk walk(a, t_first, t_end, t_step);
     float xs_next = walk.more() ? row_scale(walk.mt) : 0.f;
+    if (OUT == kScore && walk.more()) fetch_columns(walk.nt, group);
     Stat2 st{kLowest, 0.f, 0.f};
     while (walk.more()) {
       const int mt = walk.mt, nt = walk.nt;
@@ -515,6 +534,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
       const bool valid = row < a.rows;
       const float xs = xs_next;
       if (walk.more() && walk.mt != mt) xs_next = row_scale(walk.mt);
+      if constexpr (OUT == kScore) {
+        __syncwarp();  // the last tile's columns have been read
+        put_columns();
+        if (walk.more()) fetch_columns(walk.nt, group);
+      }
       if (!warp_wait(tfull_bar(acc), acc_phase, abort_flag)) {
         ok = false;
         break;
@@ -523,28 +547,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
       const uint32_t taddr =
           tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-      for (int ch = group; ch < BN / 32; ch += P::GROUPS) {
+      for (int ch = group, i = 0; ch < BN / 32; ch += P::GROUPS, ++i) {
         const int col0 = nt * BN + ch * 32;
         if (col0 >= a.N || row0 >= a.rows) break;  // warp-uniform
-        if (!have) fetch(row0, col0, buf);
-        w_s[lane] = cw;
-        b_s[lane] = OUT == kScore ? max_nan(cb * kLog2e, kMaskedWord) : cb;
-        __syncwarp();
+        const float *w_s = cols + (OUT == kScore ? i * 64 : 0), *b_s = w_s + 32;
         const int this_buf = buf;
-        buf = buf + 1 == P::BUFS ? 0 : buf + 1;
-        {
+        if constexpr (P::BUFS > 1) buf = buf + 1 == P::BUFS ? 0 : buf + 1;
+        if constexpr (OUT != kScore) {
+          if (!have) {
+            fetch_columns(nt, ch);
+            if constexpr (RES) fetch_residual(row0, col0, this_buf);
+          }
+          put_columns();
           // the next chunk: of this tile, or the first of the next one
           const bool here = ch + P::GROUPS < BN / 32 && col0 + 32 * P::GROUPS < a.N;
           const int nrow = here ? row0 : row_of(walk.mt);
-          const int ncol = here ? col0 + 32 * P::GROUPS : walk.nt * BN + group * 32;
-          have = (here || walk.more()) && nrow < a.rows && ncol < a.N;
-          if (have) fetch(nrow, ncol, buf);
+          const int nnt = here ? nt : walk.nt, nch = here ? ch + P::GROUPS : group;
+          have = (here || walk.more()) && nrow < a.rows && nnt * BN + nch * 32 < a.N;
+          if (have) {
+            fetch_columns(nnt, nch);
+            if constexpr (RES) fetch_residual(nrow, nnt * BN + nch * 32, buf);
+          }
         }
         float v[32];
         tmem_ld32(taddr + ch * 32, v);
         if constexpr (OUT == kScore) {
           score_values(v, xs, w_s, b_s, st);
-          __syncwarp();
         } else {
           lin_values(v, xs, w_s, b_s, a.relu2);
           __syncwarp();
