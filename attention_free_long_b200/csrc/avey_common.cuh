@@ -55,6 +55,26 @@ bool encode_i8_map(CUtensorMap *map, const void *base, uint64_t inner, uint64_t 
     ::avey::count_launch(name, stream);                                     \
   } while (0)
 
+// Launches `kern` so that its blocks may start while the kernel before it in the
+// stream, one of the same call, still runs.  Before its first access to global
+// memory that kernel may be writing, or still reading what this one writes,
+// `kern` calls grid_wait(); the kernel before it calls grid_release() early.
+template <typename... K, typename... A>
+inline cudaError_t launch_after(void (*kern)(K...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                                A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<K>(args)...);
+}
+
 #define AVEY_REQUIRE(cond, code, ...)   \
   do {                                  \
     if (!(cond)) {                      \
@@ -74,6 +94,12 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 __device__ __forceinline__ void record_status(int *status, int code) {
   if (status) atomicCAS(status, 0, code);
 }
+
+// Waits until the grids this one was launched after have completed and their
+// writes are visible; returns at once in a grid launched in plain stream order.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets a grid launched after this one start once every block has come here.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -337,6 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  grid_wait();  // the rows may still be on their way through the rounding kernel
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -661,6 +662,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
 
   tc_fence_before();
   __syncthreads();
+  if (OUT == kScore) grid_release();
   // Both CTAs past their loops: the pair's MMAs have drained and no remote
   // arrival is still on its way.
   cluster_sync_all();
@@ -673,7 +675,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
 
 template <int BN, int OUT, bool RES, bool ARES>
 avey_status run_linear_pair(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &o0,
-                            const CUtensorMap &o1, const CUtensorMap &r, LinArgs a, int pairs, cudaStream_t st) {
+                            const CUtensorMap &o1, const CUtensorMap &r, LinArgs a, int pairs, bool after,
+                            cudaStream_t st) {
   using P = LinLayout<BN, OUT, RES, ARES>;
   auto kern = linear_i8_pair<BN, OUT, RES, ARES>;
   const int ksteps = (a.K + kBK - 1) / kBK;
@@ -686,7 +689,16 @@ avey_status run_linear_pair(const CUtensorMap &ma, const CUtensorMap &mb, const 
     set_detail("linear_i8: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     return AVEY_ERR_CUDA;
   }
-  kern<<<2 * pairs, P::THREADS, bytes, st>>>(ma, mb, o0, o1, r, a);
+  if (after) {
+    e = launch_after(kern, 2 * pairs, P::THREADS, bytes, st, ma, mb, o0, o1, r, a);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      set_detail("linear_i8 launch failed: %s", cudaGetErrorString(e));
+      return AVEY_ERR_CUDA;
+    }
+  } else {
+    kern<<<2 * pairs, P::THREADS, bytes, st>>>(ma, mb, o0, o1, r, a);
+  }
   AVEY_CHECK_LAUNCH(OUT == kScore ? "score_i8" : "linear_i8", st);
   return AVEY_OK;
 }
@@ -697,7 +709,7 @@ inline int pairs_for(long long tiles) {
 
 template <int BN>
 avey_status run_linear_bn(const avey_linear_i8_params *p, const int8_t *xq, int64_t ld_xq, LinArgs a,
-                          void *out, avey_dtype out_dt, cudaStream_t s) {
+                          void *out, avey_dtype out_dt, bool after, cudaStream_t s) {
   CUtensorMap ma, mb, o0, o1;
   a.tiles_m = (a.rows + 255) / 256;
   a.tiles_n = (a.N + BN - 1) / BN;
@@ -720,8 +732,8 @@ avey_status run_linear_bn(const avey_linear_i8_params *p, const int8_t *xq, int6
   if (a.residual && !encode_map(&mr, true, a.residual, inner, a.rows, 1, rs, rs * a.rows, 32, 32, 128))
     return AVEY_ERR_CUDA;
   const int pairs = pairs_for(a.num_tiles);
-#define AVEY_LINEAR(OUT, ARES) run_linear_pair<BN, OUT, false, ARES>(ma, mb, o0, o1, mr, a, pairs, s)
-  if (a.residual) return run_linear_pair<BN, AVEY_F32, true, false>(ma, mb, o0, o1, mr, a, pairs, s);
+#define AVEY_LINEAR(OUT, ARES) run_linear_pair<BN, OUT, false, ARES>(ma, mb, o0, o1, mr, a, pairs, after, s)
+  if (a.residual) return run_linear_pair<BN, AVEY_F32, true, false>(ma, mb, o0, o1, mr, a, pairs, after, s);
   // fp32 outputs and pairs are bound by their stores (8192 x 768 x 8192 to fp32:
   // 61 us with x in the ring, 65 resident; to bf16: 48 and 44)
   if constexpr (BN == 256) {
@@ -740,7 +752,7 @@ inline int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
 avey_status launch_linear_i8(const avey_linear_i8_params *p, const int8_t *xq, int64_t ld_xq,
                              const float *x_scale, int rows, const float *residual, void *out,
-                             avey_dtype out_dt, int64_t ld_out, cudaStream_t s) {
+                             avey_dtype out_dt, int64_t ld_out, bool after, cudaStream_t s) {
   if (rows == 0) return AVEY_OK;
   if (linear_few_fits(rows, p->K))
     return launch_linear_few(p, xq, AVEY_I8, ld_xq, x_scale, 0, rows, residual, out, out_dt, ld_out, s);
@@ -760,9 +772,9 @@ avey_status launch_linear_i8(const avey_linear_i8_params *p, const int8_t *xq, i
   // 256 x 256 x 256: 5.5, 6.4 and 8.2; 4096 x 768 x 1536: 16.4, 12.2 and 12.4;
   // 32768 x 768 x 1536: 64, 44 and 38).
   const long long tm = (rows + 255) / 256, pairs = sm_count() / 2;
-  if (tm * ((p->N + 255) / 256) >= pairs) return run_linear_bn<256>(p, xq, ld_xq, a, out, out_dt, s);
-  if (2 * tm * ((p->N + 127) / 128) >= pairs) return run_linear_bn<128>(p, xq, ld_xq, a, out, out_dt, s);
-  return run_linear_bn<64>(p, xq, ld_xq, a, out, out_dt, s);
+  if (tm * ((p->N + 255) / 256) >= pairs) return run_linear_bn<256>(p, xq, ld_xq, a, out, out_dt, after, s);
+  if (2 * tm * ((p->N + 127) / 128) >= pairs) return run_linear_bn<128>(p, xq, ld_xq, a, out, out_dt, after, s);
+  return run_linear_bn<64>(p, xq, ld_xq, a, out, out_dt, after, s);
 }
 
 avey_status check_linear_i8(const char *fn, const avey_linear_i8_params *p, const void *x,
@@ -853,7 +865,7 @@ extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void
     st = quantize_to_ws(p, x, x_dt, ld_x, prenorm, rows, ws, &xq, &ld_xq, &xs, s);
     if (st != AVEY_OK) return st;
   }
-  return launch_linear_i8(p, xq, ld_xq, xs, rows, residual, out, out_dt, ld_out, s);
+  return launch_linear_i8(p, xq, ld_xq, xs, rows, residual, out, out_dt, ld_out, x_dt != AVEY_I8, s);
 }
 
 // ------------------------------------------------------------- scoring ------
@@ -870,6 +882,7 @@ __global__ void __launch_bounds__(256)
                const int8_t *__restrict__ Wq, long long ld_w, const int32_t *__restrict__ ids,
                float *__restrict__ logprob, float *__restrict__ stats, float *__restrict__ entropy) {
   const int row = blockIdx.x * 8 + static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  grid_wait();
   if (row >= a.rows) return;
   const int mt = row / 256;
   const long long first = static_cast<long long>(mt) * a.tiles_n, last = first + a.tiles_n - 1;
@@ -940,7 +953,7 @@ inline size_t score_partial_bytes(int rows) {
 
 avey_status launch_score_i8(const avey_linear_i8_params *p, const int8_t *xq, int64_t ld_xq,
                             const float *x_scale, int rows, const int32_t *ids, float *logprob,
-                            float *stats, float *entropy, float4 *partial, cudaStream_t s) {
+                            float *stats, float *entropy, float4 *partial, bool after, cudaStream_t s) {
   LinArgs a{};
   a.rows = rows;
   a.N = p->N;
@@ -958,10 +971,16 @@ avey_status launch_score_i8(const avey_linear_i8_params *p, const int8_t *xq, in
   if (!encode_i8_map(&ma, xq, a.K, rows, ld_xq, 128)) return AVEY_ERR_CUDA;
   if (!encode_i8_map(&mb, p->Wq, a.K, a.N, p->ld_w, 128)) return AVEY_ERR_CUDA;
   const avey_status st = a.K <= kBK * kResidentSteps
-                             ? run_linear_pair<256, kScore, false, true>(ma, mb, ma, ma, ma, a, pairs, s)
-                             : run_linear_pair<256, kScore, false, false>(ma, mb, ma, ma, ma, a, pairs, s);
+                             ? run_linear_pair<256, kScore, false, true>(ma, mb, ma, ma, ma, a, pairs, after, s)
+                             : run_linear_pair<256, kScore, false, false>(ma, mb, ma, ma, ma, a, pairs, after, s);
   if (st != AVEY_OK) return st;
-  score_join<<<(rows + 7) / 8, 256, 0, s>>>(a, pairs, xq, ld_xq, p->Wq, p->ld_w, ids, logprob, stats, entropy);
+  const cudaError_t e = launch_after(score_join, (rows + 7) / 8, 256, 0, s, a, pairs, xq, ld_xq, p->Wq, p->ld_w,
+                                     ids, logprob, stats, entropy);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    set_detail("score_join launch failed: %s", cudaGetErrorString(e));
+    return AVEY_ERR_CUDA;
+  }
   AVEY_CHECK_LAUNCH("score_join", s);
   return AVEY_OK;
 }
@@ -1014,8 +1033,8 @@ extern "C" avey_status avey_score_tokens_i8(const avey_linear_i8_params *p, cons
     }
     if (rows > kFewRows)
       return launch_score_i8(p, xq, ld_xq, xs, rows, ids, logprob, stats, entropy,
-                             reinterpret_cast<float4 *>(rest), s);
-    st = launch_linear_i8(p, xq, ld_xq, xs, rows, nullptr, logits, AVEY_F32, ld, s);
+                               reinterpret_cast<float4 *>(rest), x_dt != AVEY_I8, s);
+    st = launch_linear_i8(p, xq, ld_xq, xs, rows, nullptr, logits, AVEY_F32, ld, x_dt != AVEY_I8, s);
   }
   if (st != AVEY_OK) return st;
   return launch_token_logprobs(logits, AVEY_F32, rows, p->N, ld, ids, 0, logprob, stats, entropy, nullptr,

@@ -608,31 +608,27 @@ avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
     a.blocks *= 2;
   const int C = a.blocks;
   const int W = rows >= 8 * sms && vecs <= 1024 ? 1 : rows > 4 * sms || vecs <= 256 ? 4 : 8;
-  if (C == 1) {
-    if (W == 1)
-      token_logprobs<T, TOP, 1, false><<<(rows + 3) / 4, 128, 0, s>>>(a);
-    else if (W == 4)
-      token_logprobs<T, TOP, 4, false><<<rows, 128, 0, s>>>(a);
-    else
-      token_logprobs<T, TOP, 8, false><<<rows, 256, 0, s>>>(a);
-  } else {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows) * C);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  cfg.attrs = at;
+  if (C > 1) {
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = C;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, 8, true>, static_cast<const LpArgs>(a));
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      set_detail("token_logprobs launch failed: %s", cudaGetErrorString(e));
-      return AVEY_ERR_CUDA;
-    }
+  }
+  cfg.gridDim = dim3(W == 1 && C == 1 ? (static_cast<unsigned>(rows) + 3) / 4 : static_cast<unsigned>(rows) * C);
+  cfg.blockDim = dim3(C > 1 || W == 8 ? 256 : 128);
+  const cudaError_t e = C > 1    ? cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, 8, true>, static_cast<const LpArgs>(a))
+                        : W == 1 ? cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, 1, false>, static_cast<const LpArgs>(a))
+                        : W == 4 ? cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, 4, false>, static_cast<const LpArgs>(a))
+                                 : cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, 8, false>, static_cast<const LpArgs>(a));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    set_detail("token_logprobs launch failed: %s", cudaGetErrorString(e));
+    return AVEY_ERR_CUDA;
   }
   AVEY_CHECK_LAUNCH("token_logprobs", s);
   return AVEY_OK;
@@ -783,7 +779,8 @@ avey_status launch_token_logprobs(const void *logits, avey_dtype dt, int rows, i
   a.top_ids = top_ids;
   a.top_lp = top_lp;
   a.status = device_status_word();
-  if (dt == AVEY_F32) return top > 0 ? run_logprobs<float, true>(a, rows, s) : run_logprobs<float, false>(a, rows, s);
+  if (dt == AVEY_F32)
+    return top > 0 ? run_logprobs<float, true>(a, rows, s) : run_logprobs<float, false>(a, rows, s);
   return top > 0 ? run_logprobs<bf16, true>(a, rows, s) : run_logprobs<bf16, false>(a, rows, s);
 }
 

@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(256) quantize_rows(const void *__restrict__ x,
   constexpr int RPB = 256 / LPR, WPR = LPR / 32;  // rows per block, warps per row
   __shared__ uint32_t s_max[8];
   __shared__ float s_sum[8];
+  grid_release();  // the product that follows may prepare itself
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int me = threadIdx.x % LPR;
   const long long row = static_cast<long long>(blockIdx.x) * RPB + threadIdx.x / LPR;
