@@ -850,6 +850,16 @@ extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void
   AVEY_REQUIRE(out, AVEY_ERR_INVALID_ARG, "%s: null output", fn);
   AVEY_REQUIRE(aligned16(out) && aligned16(residual), AVEY_ERR_INVALID_ARG,
                "%s: out and residual must be 16-byte aligned", fn);
+  {
+    const uintptr_t n = static_cast<uintptr_t>(rows - 1), o = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t oes = out_dt == AVEY_F32 ? 4 : 2, xes = x_dt == AVEY_I8 ? 1 : x_dt == AVEY_F32 ? 4 : 2;
+    const uintptr_t on = (n * ld_out + p->N + (out_dt == AVEY_BF16X2 ? rows * ld_out : 0)) * oes;
+    const uintptr_t xn = (n * ld_x + p->K + (x_dt == AVEY_BF16X2 ? rows * ld_x : 0)) * xes;
+    const uintptr_t xb = reinterpret_cast<uintptr_t>(x), rb = reinterpret_cast<uintptr_t>(residual);
+    AVEY_REQUIRE(o + on <= xb || xb + xn <= o, AVEY_ERR_INVALID_ARG, "%s: out overlaps x", fn);
+    AVEY_REQUIRE(!residual || rb == o || o + on <= rb || rb + on <= o, AVEY_ERR_INVALID_ARG,
+                 "%s: out overlaps the residual without being it", fn);
+  }
   const size_t need = avey_linear_i8_workspace_bytes(x_dt, rows, p->K);
   AVEY_REQUIRE(need == 0 || (ws && (reinterpret_cast<uintptr_t>(ws) & 255) == 0), AVEY_ERR_INVALID_ARG,
                "%s: workspace must be 256-byte aligned", fn);

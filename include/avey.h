@@ -388,7 +388,8 @@ AVEY_API avey_status avey_quantize_rows(const void *x, avey_dtype dt, int rows, 
  *         avey_quantize_rows does (prenorm included) within the call; x_scale
  *         must be NULL.
  * residual [rows, N] fp32 with leading dimension ld_out, or NULL.  Needs an
- *         AVEY_F32 output, which may be the residual itself.
+ *         AVEY_F32 output and AVEY_ACT_NONE; the output may be the residual
+ *         itself.
  * out     [rows, N], leading dimension ld_out; AVEY_F32, AVEY_BF16 or
  *         AVEY_BF16X2 (lo plane rows * ld_out elements after hi).  Columns >= N
  *         are left as they were.
@@ -397,7 +398,8 @@ AVEY_API avey_status avey_quantize_rows(const void *x, avey_dtype dt, int rows, 
  * Constraints: rows >= 0 (0: nothing is done), K, N >= 1, K <= 131071 (the
  * int32 sum); ld_w % 16 == 0, ld_x % 16 == 0 for AVEY_I8, ld_out % 8 == 0;
  * Wq, w_scale, bias, out, residual and AVEY_I8 x 16-byte aligned.  out must not
- * overlap any other buffer of the call.
+ * overlap x, nor the residual unless it is the residual (both are checked), nor
+ * any other buffer of the call.
  */
 enum { AVEY_ACT_NONE = 0, AVEY_ACT_RELU2 = 1 };
 
@@ -430,14 +432,15 @@ AVEY_API size_t avey_linear_i8_workspace_bytes(avey_dtype x_dt, int rows, int K)
  *   - ids < 0: no given token, logprob 0.  ids >= V are rejected on the device
  *     (AVEY_ERR_DEVICE_BOUNDS) and treated as none.
  *   - A row of -inf alone: stats (-inf, 0), entropy 0, logprob -inf.
- *   - A row holding NaN or +inf: NaN everywhere, alternatives -1.
+ *   - A row holding NaN or +inf: NaN everywhere (logprob 0 without a given
+ *     token), alternatives -1.
  * logits  [rows, V], leading dimension ld, AVEY_F32 or AVEY_BF16, aligned to
  *         its element (rows on 16-byte boundaries are read fastest).
  * ids     [rows] int32, with logprob [rows] fp32 out; both NULL for neither.
  * stats   [rows, 2] fp32 out or NULL;  entropy [rows] fp32 out or NULL.
  * top_ids [rows, top] int32, top_logprobs [rows, top] fp32 out (top > 0).
  * Constraints: rows >= 0 (0: nothing is done), V >= 1, ld >= V, 0 <= top <= 32,
- * rows * 8 < 2^31.
+ * rows < 2^28, V <= 2^30.
  */
 AVEY_API avey_status avey_token_logprobs(const void *logits, avey_dtype dt, int rows, int V,
                                          int64_t ld, const int32_t *ids, int top, float *logprob,
@@ -465,9 +468,10 @@ AVEY_API avey_status avey_token_logprobs_backward(const void *logits, avey_dtype
 /* avey_score_tokens_i8: avey_linear_i8 against a vocabulary matrix (p->N words,
  * act AVEY_ACT_NONE), then logprob, stats and entropy of its rows as
  * avey_token_logprobs defines them, on logits that are not rounded below fp32
- * and not an output.  A bias below -1e29 counts as -inf; a logit that overflows
- * fp32 makes its row NaN.  x, x_dt, ld_x, x_scale, prenorm as avey_linear_i8;
- * outputs as avey_token_logprobs (any may be NULL, not all).
+ * and not an output.  Logits below -1e29 (a mask in the bias) may count as -inf;
+ * one that overflows fp32 may make its row NaN.  x, x_dt, ld_x, x_scale and
+ * prenorm as for avey_linear_i8; outputs as for avey_token_logprobs (any may be
+ * NULL, not all).
  * ws: at least avey_score_tokens_i8_workspace_bytes(...) bytes, 256-byte
  * aligned. */
 AVEY_API avey_status avey_score_tokens_i8(const avey_linear_i8_params *p, const void *x,

@@ -147,6 +147,54 @@ def test_score_spoilt_and_ignored_rows(cuda_dev):
         assert torch.equal(r.logprob[4:], clean.logprob[4:])
 
 
+@pytest.mark.parametrize("rows", [5, 300])
+def test_score_with_words_masked_by_the_bias(rows, cuda_dev):
+    V, d = 2100, 64
+    head = _head(V, d, cuda_dev)
+    g = torch.Generator(device=cuda_dev).manual_seed(2)
+    h = torch.randn(rows, d, device=cuda_dev, generator=g) * 3
+    free = torch.rand(V, device=cuda_dev, generator=g) < 0.3
+    free[1990:] = False  # a tile's last columns too
+    free[7] = True
+    open_words = torch.nonzero(free)[:, 0]
+    part = av.QuantLinear(head.q[open_words].contiguous(), head.scale[open_words], d, head.bias[open_words])
+    ids = torch.randint(0, open_words.numel(), (rows,), device=cuda_dev, generator=g, dtype=torch.int32)
+    want = av.avey_score_tokens_i8(h, part, ids)
+    for low in (float("-inf"), torch.finfo(torch.float32).min):
+        bias = torch.where(free, head.bias, torch.full_like(head.bias, low))
+        r = av.avey_score_tokens_i8(h, av.QuantLinear(head.q, head.scale, d, bias),
+                                    open_words[ids.long()].to(torch.int32))
+        for a, b in ((r.logprob, want.logprob), (r.stats, want.stats), (r.entropy, want.entropy)):
+            assert bool(torch.isfinite(a).all())
+            # the same terms added in another order: V / 256 + 160 roundings of sums near 1 .. 10
+            torch.testing.assert_close(a, b, rtol=200 * U, atol=200 * U)
+    none = av.QuantLinear(head.q, head.scale, d, torch.full_like(head.bias, float("-inf")))
+    r = av.avey_score_tokens_i8(h, none, ids)
+    assert bool((r.logprob == -np.inf).all()) and bool((r.entropy == 0).all())
+    assert bool((r.stats[:, 0] == -np.inf).all()) and bool((r.stats[:, 1] == 0).all())
+
+
+def test_rows_past_32_bit_offsets(cuda_dev):
+    # 2.27e9 logits: the last rows lie past 2^31 elements and 2^32 bytes
+    V, d, rows, tail = 50368, 64, 45000, 2000
+    head = _head(V, d, cuda_dev)
+    h = av.avey_quantize_rows(torch.randn(rows, d, device=cuda_dev))
+    logits = av.avey_linear_i8(h, head, out_dtype=torch.bfloat16)
+    end = av.QuantRows(h.q[-tail:].contiguous(), h.scale[-tail:].contiguous(), d)
+    last = av.avey_linear_i8(end, head, out_dtype=torch.bfloat16)
+    assert torch.equal(logits[-tail:], last)
+    ids = torch.randint(0, V, (rows,), device=cuda_dev, dtype=torch.int32)
+    r = av.avey_token_logprobs(logits, ids, top=2)
+    e = av.avey_token_logprobs(last, ids[-tail:].contiguous(), top=2)
+    for a, b in ((r.logprob, e.logprob), (r.stats, e.stats), (r.top_ids, e.top_ids)):
+        assert torch.equal(a[-tail:], b)
+    g = torch.ones(rows, device=cuda_dev)
+    dlast = av.avey_token_logprobs_backward(last, ids[-tail:].contiguous(), e, g[-tail:].contiguous())
+    av.avey_token_logprobs_backward(logits, ids, r, g, out=logits)
+    assert torch.equal(logits[-tail:], dlast)
+    assert av.device_status() == 0
+
+
 def test_encoder_to_fill_mask_and_loss(cuda_dev):
     wl, x, P, layers = _setup(cuda_dev)
     q = av.quantize_layers(layers)

@@ -7,7 +7,8 @@ import torch
 
 import attention_free_long_b200 as av
 
-A = 0x100000  # a 256-byte aligned address, never dereferenced
+A = 0x100000  # 256-byte aligned addresses, never dereferenced
+O = 0x900000
 vp = ctypes.c_void_p
 
 
@@ -41,7 +42,7 @@ def _params(**kw):
 
 
 def _linear(p=None, **kw):
-    a = dict(x=A, dt=av.AVEY_F32, ld=40, xs=None, prenorm=0, rows=40, res=None, out=A, odt=av.AVEY_F32, ldo=24,
+    a = dict(x=A, dt=av.AVEY_F32, ld=40, xs=None, prenorm=0, rows=40, res=None, out=O, odt=av.AVEY_F32, ldo=24,
              ws=A, wsb=1 << 20)
     a.update(kw)
     q = _params() if p is None else p
@@ -61,7 +62,10 @@ def _linear(p=None, **kw):
     ({}, dict(dt=av.AVEY_I8, ld=48, xs=A, prenorm=1), 1, "prenorm"),
     ({}, dict(dt=av.AVEY_I8, ld=48, xs=A, x=A + 8), 1, "aligned"),
     ({}, dict(dt=7), 2, "dtype"), ({}, dict(odt=av.AVEY_I8), 2, "output dtype"),
-    ({}, dict(ldo=20), 1, "ld_out"), ({}, dict(ldo=16), 1, "ld_out"), ({}, dict(out=A + 8), 1, "aligned"),
+    ({}, dict(ldo=20), 1, "ld_out"), ({}, dict(ldo=16), 1, "ld_out"), ({}, dict(out=O + 8), 1, "aligned"),
+    ({}, dict(out=A), 1, "overlap"), ({}, dict(out=A + 40 * 160 - 16), 1, "overlap"),
+    ({}, dict(x=O + 40 * 96 - 16), 1, "overlap"), ({}, dict(res=O + 16), 1, "overlap"),
+    ({}, dict(res=O - 16), 1, "overlap"),
     ({}, dict(res=A, odt=av.AVEY_BF16), 2, "residual"), (dict(act=1), dict(res=A), 2, "residual"),
     ({}, dict(res=A + 4), 1, "aligned"), ({}, dict(ws=None), 1, "workspace"),
     ({}, dict(ws=A + 16), 1, "workspace"), ({}, dict(wsb=64), 1, "workspace"),
