@@ -114,8 +114,8 @@ def lib() -> ctypes.CDLL:
         L.avey_compress_rows.restype = _i
         L.avey_quantize_rows.argtypes = [_vp, _i, _i, _i, _i64, _i, _vp, _i64, _vp, _vp]
         L.avey_quantize_rows.restype = _i
-        L.avey_linear_i8.argtypes = [ctypes.POINTER(LinearI8Params), _vp, _i, _i64, _vp, _i, _i, _vp, _vp,
-                                     _i, _i64, _vp, _sz, _vp]
+        L.avey_linear_i8.argtypes = [ctypes.POINTER(LinearI8Params), _vp, _i, _i64, _vp, _i, _i, _vp, _i64,
+                                     _vp, _i, _i64, _vp, _sz, _vp]
         L.avey_linear_i8.restype = _i
         L.avey_linear_i8_workspace_bytes.argtypes = [_i, _i, _i]
         L.avey_linear_i8_workspace_bytes.restype = _sz
@@ -524,20 +524,16 @@ def avey_linear_i8(x, lin: QuantLinear, act: int = AVEY_ACT_NONE,
         if rows <= 1:
             ld_out = (N + 7) // 8 * 8
     out_dt = AVEY_BF16X2 if pair else _dt(out)
+    ld_res = 0
     if residual is not None:
-        r, c, ld_r = _rows_of(residual, "residual")
+        r, c, ld_res = _rows_of(residual, "residual")
         if residual.dtype != torch.float32 or (r, c) != (rows, N):
             raise TypeError(f"residual must be fp32 [{rows}, {N}]")
-        if (rows > 1 and ld_r != ld_out) or residual.data_ptr() % 16:
-            _same_device(t, residual)
-            padded = t.new_empty((rows, ld_out), dtype=torch.float32)
-            padded[:, :N].copy_(residual)
-            residual = padded
     _same_device(t, out, residual, ws)
     need = 0 if dt == AVEY_I8 else lib().avey_linear_i8_workspace_bytes(dt, rows, lin.K)
     ws, ws_bytes = _scratch(ws, need, t)
     _call("avey_linear_i8", t, ctypes.byref(lin._params(act)), t.data_ptr(), dt, ld, _addr(scale),
-          1 if prenorm else 0, rows, _addr(residual), out.data_ptr(), out_dt, ld_out, _addr(ws), ws_bytes)
+          1 if prenorm else 0, rows, _addr(residual), ld_res, out.data_ptr(), out_dt, ld_out, _addr(ws), ws_bytes)
     return out
 
 
@@ -829,7 +825,7 @@ def _run_layers_i8(L, layers, dt, T, d, m, m_h, S, eps, prenorm, ws, st, marks):
     for li, lay in enumerate(layers):
         pu, po = lay.U._params(AVEY_ACT_RELU2), lay.O._params(AVEY_ACT_NONE)
         _check("avey_linear_i8", L.avey_linear_i8(
-            ctypes.byref(pu), _ptr(cur), AVEY_F32, d, None, int(bool(prenorm)), T, None, z, AVEY_BF16X2, m,
+            ctypes.byref(pu), _ptr(cur), AVEY_F32, d, None, int(bool(prenorm)), T, None, 0, z, AVEY_BF16X2, m,
             q, q_bytes, st))
         tail = ctypes.c_void_p(z + 2 * m_h)
         if lay.kind == AVEY_STATIC:
@@ -839,7 +835,7 @@ def _run_layers_i8(L, layers, dt, T, d, m, m_h, S, eps, prenorm, ws, st, marks):
             _check("avey_dynamic_mix", L.avey_dynamic_mix(tail, m, AVEY_BF16X2, T // S, S, m - m_h, eps, tail,
                                                           m, st))
         _check("avey_linear_i8", L.avey_linear_i8(
-            ctypes.byref(po), z, AVEY_BF16X2, m, None, 0, T, _ptr(cur), _ptr(nxt), AVEY_F32, d, q, q_bytes,
+            ctypes.byref(po), z, AVEY_BF16X2, m, None, 0, T, _ptr(cur), d, _ptr(nxt), AVEY_F32, d, q, q_bytes,
             st))
         if marks is not None:
             marks[3 + li].record()

@@ -122,8 +122,8 @@ avey_status check_linear_i8(const char *fn, const avey_linear_i8_params *p, cons
 // after: the kernel before it in the stream is launch_quantize_rows of the same
 // call (see launch_after).
 avey_status launch_linear_i8(const avey_linear_i8_params *p, const int8_t *xq, int64_t ld_xq,
-                             const float *x_scale, int rows, const float *residual, void *out,
-                             avey_dtype out_dt, int64_t ld_out, bool after, cudaStream_t s);
+                             const float *x_scale, int rows, const float *residual, int64_t ld_res,
+                             void *out, avey_dtype out_dt, int64_t ld_out, bool after, cudaStream_t s);
 // The same for few rows (avey_linear_few.cu): whether the kernel takes this many
 // rows of K values, whether it also quantises them, and the product.  x of type
 // AVEY_I8 comes with x_scale, other types without.
@@ -132,7 +132,8 @@ bool linear_few_fits(int rows, int K);
 bool linear_few_quantizes(avey_dtype x_dt, int rows, int K);
 avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt, int64_t ld_x,
                               const float *x_scale, int prenorm, int rows, const float *residual,
-                              void *out, avey_dtype out_dt, int64_t ld_out, cudaStream_t s);
+                              int64_t ld_res, void *out, avey_dtype out_dt, int64_t ld_out,
+                              cudaStream_t s);
 // Arguments as avey_token_logprobs, checked by the caller (avey_logprobs.cu).
 avey_status launch_token_logprobs(const void *logits, avey_dtype dt, int rows, int V, int64_t ld,
                                   const int32_t *ids, int top, float *logprob, float *stats,

@@ -31,6 +31,7 @@ struct FewArgs {
   const int8_t *Wq;
   long long ld_w;
   const float *w_scale, *bias, *residual;
+  long long ld_res;
   int relu2;
   void *out;
   long long ld_out;
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(WARPS * 32) linear_i8_few(const FewArgs a) {
         }
         const long long at = t * a.ld_out + n;
         if constexpr (OUT == AVEY_F32) {
-          if (a.residual) y += a.residual[at];
+          if (a.residual) y += a.residual[t * a.ld_res + n];
           static_cast<float *>(a.out)[at] = y;
         } else {
           bf16 *hi = static_cast<bf16 *>(a.out) + at;
@@ -242,7 +243,8 @@ bool linear_few_quantizes(avey_dtype x_dt, int rows, int K) {
 
 avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt, int64_t ld_x,
                               const float *x_scale, int prenorm, int rows, const float *residual,
-                              void *out, avey_dtype out_dt, int64_t ld_out, cudaStream_t s) {
+                              int64_t ld_res, void *out, avey_dtype out_dt, int64_t ld_out,
+                              cudaStream_t s) {
   FewArgs a{};
   a.x = x;
   a.ld_x = ld_x;
@@ -258,6 +260,7 @@ avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, ave
   a.w_scale = p->w_scale;
   a.bias = p->bias;
   a.residual = residual;
+  a.ld_res = ld_res;
   a.relu2 = p->act == AVEY_ACT_RELU2;
   a.out = out;
   a.ld_out = ld_out;

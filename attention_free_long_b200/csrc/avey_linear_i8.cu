@@ -96,6 +96,8 @@ struct LinArgs {
   const float *x_scale, *w_scale, *bias;
   int relu2;
   const float *residual;
+  long long ld_res;
+  int res_tma;  // the residual's rows lie on 16-byte boundaries
   // TMA stores write whole 16-byte pieces: they cover the columns < N_tma, and
   // plain stores through out the rest of a row
   int N_tma;
@@ -180,7 +182,7 @@ __device__ __forceinline__ void store_rest(const LinArgs &a, int row, int col0, 
     const int c = col0 + j;
     if (c < a.N_tma || c >= a.N) continue;
     if constexpr (OUT == AVEY_F32) {
-      static_cast<float *>(a.out)[at + c] = RES ? v[j] + a.residual[at + c] : v[j];
+      static_cast<float *>(a.out)[at + c] = RES && a.res_tma ? v[j] + a.residual[row * a.ld_res + c] : v[j];
     } else {
       bf16 *hi = static_cast<bf16 *>(a.out) + at + c;
       *hi = __float2bfloat16_rn(v[j]);
@@ -512,7 +514,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
     // The residual of a chunk into staging buffer `to`, a chunk ahead.
     uint32_t coming = 0;  // buffers with a copy in flight
     auto fetch_residual = [&](int row0, int col0, int to) {
-      if (col0 >= a.N_tma) return;
+      if (col0 >= a.N_tma || !a.res_tma) return;
       if (lane == 0) {
         bulk_wait_read<1>();  // the store from this buffer, three chunks ago at least, has read it
         mbar_arrive_expect_tx(res_bar(ew, to), P::BUF);
@@ -577,10 +579,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
         } else {
           lin_values(v, xs, w_s, b_s, a.relu2);
           __syncwarp();
+          if (RES && !a.res_tma && valid) {
+            const float *r = a.residual + row * a.ld_res;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col0 + j < a.N) v[j] += r[col0 + j];
+          }
           if (col0 + 32 > a.N_tma && valid) store_rest<OUT, RES>(a, row, col0, v);
           if (col0 < a.N_tma) {  // warp-uniform
             const uint32_t at = stg + this_buf * P::BUF;
-            if constexpr (RES) {
+            if (RES && a.res_tma) {
               if (!warp_wait(res_bar(ew, this_buf), res_phase >> this_buf & 1u, abort_flag)) {
                 ok = false;
                 break;
@@ -729,7 +737,9 @@ avey_status run_linear_bn(const avey_linear_i8_params *p, const int8_t *xq, int6
                   a.rows, 1, rs, rs * a.rows, 32, 32, 64))
     return AVEY_ERR_CUDA;
   CUtensorMap mr = o0;
-  if (a.residual && !encode_map(&mr, true, a.residual, inner, a.rows, 1, rs, rs * a.rows, 32, 32, 128))
+  const uint64_t res_rs = static_cast<uint64_t>(a.ld_res) * 4;
+  a.res_tma = a.residual && aligned16(a.residual) && res_rs % 16 == 0;
+  if (a.res_tma && !encode_map(&mr, true, a.residual, inner, a.rows, 1, res_rs, res_rs * a.rows, 32, 32, 128))
     return AVEY_ERR_CUDA;
   const int pairs = pairs_for(a.num_tiles);
 #define AVEY_LINEAR(OUT, ARES) run_linear_pair<BN, OUT, false, ARES>(ma, mb, o0, o1, mr, a, pairs, after, s)
@@ -751,11 +761,11 @@ inline int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 }  // namespace
 
 avey_status launch_linear_i8(const avey_linear_i8_params *p, const int8_t *xq, int64_t ld_xq,
-                             const float *x_scale, int rows, const float *residual, void *out,
-                             avey_dtype out_dt, int64_t ld_out, bool after, cudaStream_t s) {
+                             const float *x_scale, int rows, const float *residual, int64_t ld_res,
+                             void *out, avey_dtype out_dt, int64_t ld_out, bool after, cudaStream_t s) {
   if (rows == 0) return AVEY_OK;
   if (linear_few_fits(rows, p->K))
-    return launch_linear_few(p, xq, AVEY_I8, ld_xq, x_scale, 0, rows, residual, out, out_dt, ld_out, s);
+    return launch_linear_few(p, xq, AVEY_I8, ld_xq, x_scale, 0, rows, residual, ld_res, out, out_dt, ld_out, s);
   LinArgs a{};
   a.rows = rows;
   a.N = p->N;
@@ -765,6 +775,7 @@ avey_status launch_linear_i8(const avey_linear_i8_params *p, const int8_t *xq, i
   a.bias = p->bias;
   a.relu2 = p->act == AVEY_ACT_RELU2;
   a.residual = residual;
+  a.ld_res = ld_res;
   a.ld_out = ld_out;
   a.status = device_status_word();
   // The widest tile that gives every pair of SMs one, 128 columns down to every
@@ -834,8 +845,9 @@ extern "C" size_t avey_linear_i8_workspace_bytes(avey_dtype x_dt, int rows, int 
 
 extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt,
                                       int64_t ld_x, const float *x_scale, int prenorm, int rows,
-                                      const float *residual, void *out, avey_dtype out_dt,
-                                      int64_t ld_out, void *ws, size_t ws_bytes, avey_stream_t stream) {
+                                      const float *residual, int64_t ld_res, void *out,
+                                      avey_dtype out_dt, int64_t ld_out, void *ws, size_t ws_bytes,
+                                      avey_stream_t stream) {
   const char *fn = "avey_linear_i8";
   avey_status st = check_linear_i8(fn, p, x, x_dt, ld_x, x_scale, prenorm, rows);
   if (st != AVEY_OK) return st;
@@ -846,10 +858,12 @@ extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void
   AVEY_REQUIRE(!residual || out_dt == AVEY_F32, AVEY_ERR_UNSUPPORTED, "%s: a residual needs an F32 output", fn);
   AVEY_REQUIRE(!residual || p->act == AVEY_ACT_NONE, AVEY_ERR_UNSUPPORTED,
                "%s: a residual goes with AVEY_ACT_NONE", fn);
+  AVEY_REQUIRE(!residual || ld_res >= p->N, AVEY_ERR_INVALID_ARG, "%s: ld_res=%lld < N=%d", fn,
+               static_cast<long long>(ld_res), p->N);
   if (rows == 0) return AVEY_OK;
   AVEY_REQUIRE(out, AVEY_ERR_INVALID_ARG, "%s: null output", fn);
-  AVEY_REQUIRE(aligned16(out) && aligned16(residual), AVEY_ERR_INVALID_ARG,
-               "%s: out and residual must be 16-byte aligned", fn);
+  AVEY_REQUIRE(aligned16(out) && (reinterpret_cast<uintptr_t>(residual) & 3) == 0, AVEY_ERR_INVALID_ARG,
+               "%s: out must be 16-byte and the residual 4-byte aligned", fn);
   {
     const uintptr_t n = static_cast<uintptr_t>(rows - 1), o = reinterpret_cast<uintptr_t>(out);
     const uintptr_t oes = out_dt == AVEY_F32 ? 4 : 2, xes = x_dt == AVEY_I8 ? 1 : x_dt == AVEY_F32 ? 4 : 2;
@@ -857,7 +871,9 @@ extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void
     const uintptr_t xn = (n * ld_x + p->K + (x_dt == AVEY_BF16X2 ? rows * ld_x : 0)) * xes;
     const uintptr_t xb = reinterpret_cast<uintptr_t>(x), rb = reinterpret_cast<uintptr_t>(residual);
     AVEY_REQUIRE(o + on <= xb || xb + xn <= o, AVEY_ERR_INVALID_ARG, "%s: out overlaps x", fn);
-    AVEY_REQUIRE(!residual || rb == o || o + on <= rb || rb + on <= o, AVEY_ERR_INVALID_ARG,
+    const uintptr_t rn = (n * ld_res + p->N) * 4;
+    AVEY_REQUIRE(!residual || (rb == o && (ld_res == ld_out || rows == 1)) || o + on <= rb || rb + rn <= o,
+                 AVEY_ERR_INVALID_ARG,
                  "%s: out overlaps the residual without being it", fn);
   }
   const size_t need = avey_linear_i8_workspace_bytes(x_dt, rows, p->K);
@@ -867,7 +883,7 @@ extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void
                need);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (linear_few_quantizes(x_dt, rows, p->K))
-    return launch_linear_few(p, x, x_dt, ld_x, nullptr, prenorm ? 1 : 0, rows, residual, out, out_dt, ld_out, s);
+    return launch_linear_few(p, x, x_dt, ld_x, nullptr, prenorm ? 1 : 0, rows, residual, ld_res, out, out_dt, ld_out, s);
   const int8_t *xq = static_cast<const int8_t *>(x);
   const float *xs = x_scale;
   int64_t ld_xq = ld_x;
@@ -875,7 +891,7 @@ extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void
     st = quantize_to_ws(p, x, x_dt, ld_x, prenorm, rows, ws, &xq, &ld_xq, &xs, s);
     if (st != AVEY_OK) return st;
   }
-  return launch_linear_i8(p, xq, ld_xq, xs, rows, residual, out, out_dt, ld_out, x_dt != AVEY_I8, s);
+  return launch_linear_i8(p, xq, ld_xq, xs, rows, residual, ld_res, out, out_dt, ld_out, x_dt != AVEY_I8, s);
 }
 
 // ------------------------------------------------------------- scoring ------
@@ -1032,7 +1048,7 @@ extern "C" avey_status avey_score_tokens_i8(const avey_linear_i8_params *p, cons
   float *logits = reinterpret_cast<float *>(rest);
   const int64_t ld = score_ld(p->N);
   if (linear_few_quantizes(x_dt, rows, p->K)) {
-    st = launch_linear_few(p, x, x_dt, ld_x, nullptr, prenorm ? 1 : 0, rows, nullptr, logits, AVEY_F32, ld, s);
+    st = launch_linear_few(p, x, x_dt, ld_x, nullptr, prenorm ? 1 : 0, rows, nullptr, 0, logits, AVEY_F32, ld, s);
   } else {
     const int8_t *xq = static_cast<const int8_t *>(x);
     const float *xs = x_scale;
@@ -1044,7 +1060,7 @@ extern "C" avey_status avey_score_tokens_i8(const avey_linear_i8_params *p, cons
     if (rows > kFewRows)
       return launch_score_i8(p, xq, ld_xq, xs, rows, ids, logprob, stats, entropy,
                                reinterpret_cast<float4 *>(rest), x_dt != AVEY_I8, s);
-    st = launch_linear_i8(p, xq, ld_xq, xs, rows, nullptr, logits, AVEY_F32, ld, x_dt != AVEY_I8, s);
+    st = launch_linear_i8(p, xq, ld_xq, xs, rows, nullptr, 0, logits, AVEY_F32, ld, x_dt != AVEY_I8, s);
   }
   if (st != AVEY_OK) return st;
   return launch_token_logprobs(logits, AVEY_F32, rows, p->N, ld, ids, 0, logprob, stats, entropy, nullptr,

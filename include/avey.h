@@ -387,9 +387,10 @@ AVEY_API avey_status avey_quantize_rows(const void *x, avey_dtype dt, int rows, 
  *         x_scale [rows].  AVEY_F32, AVEY_BF16, AVEY_BF16X2: quantised as
  *         avey_quantize_rows does (prenorm included) within the call; x_scale
  *         must be NULL.
- * residual [rows, N] fp32 with leading dimension ld_out, or NULL.  Needs an
- *         AVEY_F32 output and AVEY_ACT_NONE; the output may be the residual
- *         itself.
+ * residual [rows, N] fp32, leading dimension ld_res, or NULL.  Needs an AVEY_F32
+ *         output and AVEY_ACT_NONE; the output may be the residual itself (with
+ *         the same leading dimension).  Rows on 16-byte boundaries are read
+ *         fastest.
  * out     [rows, N], leading dimension ld_out; AVEY_F32, AVEY_BF16 or
  *         AVEY_BF16X2 (lo plane rows * ld_out elements after hi).  Columns >= N
  *         are left as they were.
@@ -397,7 +398,7 @@ AVEY_API avey_status avey_quantize_rows(const void *x, avey_dtype dt, int rows, 
  *         (may be NULL when that is 0).
  * Constraints: rows >= 0 (0: nothing is done), K, N >= 1, K <= 131071 (the
  * int32 sum); ld_w % 16 == 0, ld_x % 16 == 0 for AVEY_I8, ld_out % 8 == 0;
- * Wq, w_scale, bias, out, residual and AVEY_I8 x 16-byte aligned.  out must not
+ * ld_res >= N; Wq, w_scale, bias, out and AVEY_I8 x 16-byte aligned.  out must not
  * overlap x, nor the residual unless it is the residual (both are checked), nor
  * any other buffer of the call.
  */
@@ -414,8 +415,9 @@ typedef struct {
 
 AVEY_API avey_status avey_linear_i8(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt,
                                     int64_t ld_x, const float *x_scale, int prenorm, int rows,
-                                    const float *residual, void *out, avey_dtype out_dt,
-                                    int64_t ld_out, void *ws, size_t ws_bytes, avey_stream_t stream);
+                                    const float *residual, int64_t ld_res, void *out,
+                                    avey_dtype out_dt, int64_t ld_out, void *ws, size_t ws_bytes,
+                                    avey_stream_t stream);
 
 AVEY_API size_t avey_linear_i8_workspace_bytes(avey_dtype x_dt, int rows, int K);
 

@@ -190,6 +190,11 @@ def test_residual_alone_and_in_place(rows, K, N, cuda_dev):
     y, err = _product(x, q, w, b, 0, res)
     got = av.avey_linear_i8(t, lin, residual=r)
     assert (np.abs(got.double().cpu().numpy() - y) <= err).all()
+    # rows of the residual that start anywhere
+    loose = torch.full((rows * (N + 3) + 8,), float("nan"), device=cuda_dev)
+    view = loose[1:1 + rows * (N + 3)].view(rows, N + 3)[:, :N]
+    view.copy_(r)
+    assert torch.equal(av.avey_linear_i8(t, lin, residual=view), got)
     ld = (N + 7) // 8 * 8
     wide = torch.full((rows + 2, ld + 8), 7.0, device=cuda_dev)  # rows and columns around the output
     wide[:rows, :N] = r

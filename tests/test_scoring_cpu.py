@@ -42,12 +42,12 @@ def _params(**kw):
 
 
 def _linear(p=None, **kw):
-    a = dict(x=A, dt=av.AVEY_F32, ld=40, xs=None, prenorm=0, rows=40, res=None, out=O, odt=av.AVEY_F32, ldo=24,
+    a = dict(x=A, dt=av.AVEY_F32, ld=40, xs=None, prenorm=0, rows=40, res=None, ldr=24, out=O, odt=av.AVEY_F32, ldo=24,
              ws=A, wsb=1 << 20)
     a.update(kw)
     q = _params() if p is None else p
     return av.lib().avey_linear_i8(ctypes.byref(q), a["x"], a["dt"], a["ld"], a["xs"], a["prenorm"], a["rows"],
-                                   a["res"], a["out"], a["odt"], a["ldo"], a["ws"], a["wsb"], None)
+                                   a["res"], a["ldr"], a["out"], a["odt"], a["ldo"], a["ws"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("pk,kw,code,word", [
@@ -67,7 +67,7 @@ def _linear(p=None, **kw):
     ({}, dict(x=O + 40 * 96 - 16), 1, "overlap"), ({}, dict(res=O + 16), 1, "overlap"),
     ({}, dict(res=O - 16), 1, "overlap"),
     ({}, dict(res=A, odt=av.AVEY_BF16), 2, "residual"), (dict(act=1), dict(res=A), 2, "residual"),
-    ({}, dict(res=A + 4), 1, "aligned"), ({}, dict(ws=None), 1, "workspace"),
+    ({}, dict(res=A + 2), 1, "aligned"), ({}, dict(res=A, ldr=23), 1, "ld_res"), ({}, dict(res=O, ldr=32), 1, "overlap"), ({}, dict(ws=None), 1, "workspace"),
     ({}, dict(ws=A + 16), 1, "workspace"), ({}, dict(wsb=64), 1, "workspace"),
 ])
 def test_linear_i8_refuses(pk, kw, code, word):
@@ -76,7 +76,7 @@ def test_linear_i8_refuses(pk, kw, code, word):
 
 def test_linear_i8_refuses_null_params_and_sizes_its_workspace():
     L = av.lib()
-    assert L.avey_linear_i8(None, A, 0, 40, None, 0, 4, None, A, 0, 24, A, 1 << 20, None) == 1
+    assert L.avey_linear_i8(None, A, 0, 40, None, 0, 4, None, 0, A, 0, 24, A, 1 << 20, None) == 1
     assert L.avey_linear_i8_workspace_bytes(av.AVEY_I8, 100, 40) == 0
     assert L.avey_linear_i8_workspace_bytes(av.AVEY_F32, 0, 40) == 0
     # few rows are rounded by the product's own kernel
