@@ -9,7 +9,7 @@
 //
 // What bounds it: long contractions the tensor pipe (8192^3 to bf16 runs at 3.0
 // POP/s, 0.97 of what the pipe does at the 1.33 GHz that the power cap leaves it);
-// short ones the epilogue, which has 3072 tensor cycles a tile of K = 768 to get
+// short ones the epilogue, which has about 3100 tensor cycles a tile of K = 768 to get
 // 32768 sums out of TMEM and takes about 5000.  Up to K = 1024 a pair keeps its
 // 256 rows of x in shared memory and walks the channels (ARES): half the bytes
 // from L2 and into shared memory, 44 instead of 48 us for 8192 x 768 x 8192 to
