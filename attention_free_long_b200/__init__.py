@@ -547,6 +547,21 @@ class TokenLogprobs:
     top_logprobs: Optional[torch.Tensor] = None  # fp32 [rows, top]
 
 
+def _score_outputs(t: torch.Tensor, rows: int, given: bool, top: int) -> TokenLogprobs:
+    """The outputs of one call, in one allocation on t's device."""
+    buf = t.new_empty(((4 if given else 3) * rows + 2 * top * rows,), dtype=torch.float32)
+    row = (1,)
+    r = TokenLogprobs(None, buf.as_strided((rows, 2), (2, 1), 0), buf.as_strided((rows,), row, 2 * rows))
+    at = 3 * rows
+    if given:
+        r.logprob = buf.as_strided((rows,), row, at)
+        at += rows
+    if top:
+        r.top_logprobs = buf.as_strided((rows, top), (top, 1), at)
+        r.top_ids = buf.view(torch.int32).as_strided((rows, top), (top, 1), at + top * rows)
+    return r
+
+
 def avey_token_logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None,
                         top: int = 0) -> TokenLogprobs:
     """Log probabilities of ids (int32 [rows], negative: none) under logits
@@ -559,17 +574,10 @@ def avey_token_logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None
     dt = _dt(logits)
     _vector(ids, "ids", rows, torch.int32)
     _same_device(logits, ids)
-    f32 = torch.float32
-    stats, entropy = logits.new_empty((rows, 2), dtype=f32), logits.new_empty((rows,), dtype=f32)
-    logprob = top_ids = top_lp = None
-    if ids is not None:
-        logprob = logits.new_empty((rows,), dtype=f32)
-    if top > 0:
-        top_ids = logits.new_empty((rows, top), dtype=torch.int32)
-        top_lp = logits.new_empty((rows, top), dtype=f32)
-    _call("avey_token_logprobs", logits, logits.data_ptr(), dt, rows, V, ld, _addr(ids), top, _addr(logprob),
-          stats.data_ptr(), entropy.data_ptr(), _addr(top_ids), _addr(top_lp))
-    return TokenLogprobs(logprob, stats, entropy, top_ids, top_lp)
+    r = _score_outputs(logits, rows, ids is not None, top if top > 0 else 0)
+    _call("avey_token_logprobs", logits, logits.data_ptr(), dt, rows, V, ld, _addr(ids), top,
+          _addr(r.logprob), r.stats.data_ptr(), r.entropy.data_ptr(), _addr(r.top_ids), _addr(r.top_logprobs))
+    return r
 
 
 def avey_token_logprobs_backward(logits: torch.Tensor, ids: Optional[torch.Tensor], scores: TokenLogprobs,
@@ -615,15 +623,13 @@ def avey_score_tokens_i8(x, head: QuantLinear, ids: Optional[torch.Tensor] = Non
     t, dt, rows, ld, scale = _linear_input(x, head)
     _vector(ids, "ids", rows, torch.int32)
     _same_device(t, ids, ws)
-    f32 = torch.float32
-    logprob = None if ids is None else t.new_empty((rows,), dtype=f32)
-    stats, entropy = t.new_empty((rows, 2), dtype=f32), t.new_empty((rows,), dtype=f32)
+    r = _score_outputs(t, rows, ids is not None, 0)
     need = lib().avey_score_tokens_i8_workspace_bytes(rows, head.K, head.q.shape[0])
     ws, ws_bytes = _scratch(ws, need, t)
     _call("avey_score_tokens_i8", t, ctypes.byref(head._params(AVEY_ACT_NONE)), t.data_ptr(), dt, ld,
-          _addr(scale), 1 if prenorm else 0, rows, _addr(ids), _addr(logprob), stats.data_ptr(),
-          entropy.data_ptr(), _addr(ws), ws_bytes)
-    return TokenLogprobs(logprob, stats, entropy)
+          _addr(scale), 1 if prenorm else 0, rows, _addr(ids), _addr(r.logprob), r.stats.data_ptr(),
+          r.entropy.data_ptr(), _addr(ws), ws_bytes)
+    return r
 
 
 # ------------------------------------------------------------------ layer --

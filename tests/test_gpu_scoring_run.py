@@ -224,6 +224,22 @@ def test_encoder_to_fill_mask_and_loss(cuda_dev):
     assert av.device_status() == 0
 
 
+@pytest.mark.parametrize("world", [2, 3])
+def test_sequence_shares_of_8_bit_layers(world, cuda_dev):
+    wl, x, P, layers = _setup(cuda_dev, S=64, N=1000, B=2)
+    q = av.quantize_layers(layers)
+    full = av.encoder_forward(x, P, q, wl.S, wl.k, wl.m_h, wl.eps, wl.prenorm)
+    _, _, scores = av.avey_rank(x, wl.S, wl.k, return_scores=True)
+    n = scores.shape[1]
+    for rank in range(world):
+        # the sum over the ranks is the whole matrix
+        out = av.encoder_forward_sharded(x, P, q, wl.S, wl.k, wl.m_h, wl.eps, wl.prenorm, rank, world,
+                                         lambda s: s.copy_(scores))
+        t0, t1 = av.shard_targets(n, world, rank)
+        assert torch.equal(out, full[:, t0 * wl.S:t1 * wl.S])
+    assert av.device_status() == 0
+
+
 def test_captured_run(cuda_dev):
     wl, x, P, layers = _setup(cuda_dev, N=640)
     q = av.quantize_layers(layers)
