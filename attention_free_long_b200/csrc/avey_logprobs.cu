@@ -6,14 +6,17 @@
 //
 // Forward: one pass over the row with a running maximum; each thread carries
 // (m, s, t) = (max, sum e, sum e (x - m)) and rescales s and t once a batch
-// when its maximum grows.  A row belongs to one block, or to a cluster of up to eight blocks when there are
-// few rows, whose partial results meet in distributed shared memory.
+// when its maximum grows.  A row belongs to one warp, to one block, or, when there
+// are few rows, to a cluster of up to eight blocks, whose partial results meet in
+// distributed shared memory.
 // Alternatives: the `top`-th largest of the threads' maxima is a bar that `top`
 // elements reach, so every alternative reaches it and lies with a thread whose
 // maximum does: about `top` of them.  A thread knows which batch its maximum
 // came from and the largest maximum of its other batches; mostly that one is
 // below the bar, and eight vectors of the thread are read a second time, four
-// threads' at once.  What reaches the bar goes through sorted lists, one a warp.
+// threads' at once.  What reaches the bar waits in a queue, one a warp, whose 32
+// oldest entries are sorted and merged into the warp's list together; the list's
+// `top`-th then raises the bar.
 // Backward: dx_j = g (1[j = id] - p_j) - h p_j (log p_j + entropy), one read and
 // one write of the row.
 #include <algorithm>
@@ -26,7 +29,6 @@ namespace avey {
 namespace {
 
 constexpr int kLpThreads = 256;       // threads of the gradient's blocks
-constexpr int kBatch = 8;             // 16-byte vectors a thread takes at once
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
 // exp(d) is 0 in fp32 from here down; keeps 0 * (x - m) finite
@@ -78,16 +80,18 @@ struct Vec<float> {
   static __device__ __forceinline__ float max(const uint4 &w) {
     return fmaxf(max3f(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z)), __uint_as_float(w.w));
   }
-  static __device__ __forceinline__ float max_all(const uint4 *w) {
+  template <int B>
+  static __device__ __forceinline__ float max_all(const uint4 (&w)[B]) {
     float m = max(w[0]);
 #pragma unroll
-    for (int i = 1; i < kBatch; ++i) m = fmaxf(m, max(w[i]));
+    for (int i = 1; i < B; ++i) m = fmaxf(m, max(w[i]));
     return m;
   }
-  static __device__ __forceinline__ float min_all(const uint4 *w) {
+  template <int B>
+  static __device__ __forceinline__ float min_all(const uint4 (&w)[B]) {
     float m = INFINITY;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+    for (int i = 0; i < B; ++i)
       m = min3f(min3f(m, __uint_as_float(w[i].x), __uint_as_float(w[i].y)), __uint_as_float(w[i].z),
                 __uint_as_float(w[i].w));
     return m;
@@ -119,17 +123,19 @@ struct Vec<bf16> {
     const __nv_bfloat162 m = __hmax2(__hmax2(b2(w.x), b2(w.y)), __hmax2(b2(w.z), b2(w.w)));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  static __device__ __forceinline__ float max_all(const uint4 *w) {
+  template <int B>
+  static __device__ __forceinline__ float max_all(const uint4 (&w)[B]) {
     __nv_bfloat162 m = b2(w[0].x);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+    for (int i = 0; i < B; ++i)
       m = __hmax2(__hmax2(__hmax2(m, b2(w[i].x)), b2(w[i].y)), __hmax2(b2(w[i].z), b2(w[i].w)));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  static __device__ __forceinline__ float min_all(const uint4 *w) {
+  template <int B>
+  static __device__ __forceinline__ float min_all(const uint4 (&w)[B]) {
     __nv_bfloat162 m = b2(w[0].x);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+    for (int i = 0; i < B; ++i)
       m = __hmin2(__hmin2(__hmin2(m, b2(w[i].x)), b2(w[i].y)), __hmin2(b2(w[i].z), b2(w[i].w)));
     return fminf(__low2float(m), __high2float(m));
   }
@@ -210,9 +216,10 @@ struct Best {
 };
 
 // A batch of vectors u, u + stride, .. into a thread's statistics; s and t are
-// the running sums.
-template <typename T, bool TOP>
-__device__ __forceinline__ void add_batch(const uint4 (&w)[kBatch], int u, Stat &st, float2 &s, float2 &t, Best &best) {
+// the running sums.  PART: n of them, the others are -inf.
+template <typename T, bool TOP, bool PART, int B>
+__device__ __forceinline__ void add_batch(const uint4 (&w)[B], int u, int n, Stat &st, float2 &s, float2 &t,
+                                          Best &best) {
   const float top = Vec<T>::max_all(w);
   if constexpr (TOP) {
     best.second = fmaxf(best.second, fminf(best.first, top));
@@ -226,27 +233,43 @@ __device__ __forceinline__ void add_batch(const uint4 (&w)[kBatch], int u, Stat 
     s = make_float2(st.s, 0.f);
     t = make_float2(st.t, 0.f);
   }
-  if (Vec<T>::min_all(w) >= kLow) {
+  if constexpr (PART) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) add_terms<T, false>(w[i], st.m, s, t);
+    for (int i = 0; i < B; ++i)
+      if (i < n) add_terms<T, true>(w[i], st.m, s, t);
+  } else if (Vec<T>::min_all(w) >= kLow) {
+#pragma unroll
+    for (int i = 0; i < B; ++i) add_terms<T, false>(w[i], st.m, s, t);
   } else {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) add_terms<T, true>(w[i], st.m, s, t);
+    for (int i = 0; i < B; ++i) add_terms<T, true>(w[i], st.m, s, t);
   }
 }
 
-
-// Descending sort of one value per lane.
-__device__ __forceinline__ uint32_t warp_sort(uint32_t v, int lane) {
+// Descending sort of the first n lanes' values; the other lanes hold 0.
+template <typename K>
+__device__ __forceinline__ K warp_sort(K v, int n, int lane) {
 #pragma unroll
   for (int k = 2; k <= 32; k <<= 1) {
+    if (k > 2 && n <= k / 2) break;
 #pragma unroll
     for (int j = k >> 1; j > 0; j >>= 1) {
-      const uint32_t o = __shfl_xor_sync(0xffffffffu, v, j);
+      const K o = __shfl_xor_sync(0xffffffffu, v, j);
       v = ((lane & j) == 0) == ((lane & k) == 0) ? max(v, o) : min(v, o);
     }
   }
   return v;
+}
+// The `top` largest of the lanes' values, descending over the lanes (then any).
+__device__ __forceinline__ uint32_t warp_largest(uint32_t v, int top, int lane) {
+  if (top > 4) return warp_sort(v, 32, lane);
+  uint32_t r = 0;
+  for (int i = 0; i < top; ++i) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, v);
+    if (lane == i) r = m;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, v == m)) - 1) v = 0;
+  }
+  return r;
 }
 
 // The L largest of two descending lists of L lanes each, descending; o is the
@@ -367,69 +390,107 @@ __device__ __forceinline__ float given_logit(const LpArgs &a, const Row<T> &r, i
   return id >= 0 ? Vec<T>::to_f(r.p[id]) : 0.f;
 }
 
-// A vector's elements of at least `bar`, one vector per lane from element e0,
-// into the warp's descending list of 32 keys over the lanes.
-template <typename T>
-__device__ __forceinline__ void insert_top(const uint4 &w, bool in, uint32_t e0, float bar, uint64_t &list, int lane) {
-  constexpr int N = Vec<T>::N;
-  uint32_t lanes = __ballot_sync(0xffffffffu, in && Vec<T>::max(w) >= bar);
-  if (lanes == 0) return;
-  float v[N];
-  uint32_t want = 0;
-  Vec<T>::unpack(w, v);
-#pragma unroll
-  for (int j = 0; j < N; ++j)
-    if (in && v[j] >= bar && v[j] > -INFINITY) want |= 1u << j;
-  if (__popc(lanes) > 4) {
-    // many equal values: only those that would still enter the list
-    const uint64_t full = __shfl_sync(0xffffffffu, list, 31);
+// A warp's candidates: the largest 32 sorted so far, and those still in line.
+struct Select {
+  uint64_t *queue;  // 64 keys of this warp
+  uint64_t list;    // lane i: the i-th largest, 0 for none
+  float bar;        // at least `top` elements of the row reach it
+  int top, lane, waiting;
+  bool none;  // the list is empty
+
+  // The first 32 of the queue into the list.
+  __device__ __forceinline__ void merge(int count) {
+    __syncwarp();
+    const uint64_t key = warp_sort(lane < count ? queue[lane] : 0ull, count, lane);
+    // zeros behind it: reversed they meet the end of the list
+    list = none ? key : merge_reversed<32>(list, __shfl_xor_sync(0xffffffffu, key, 31), lane);
+    none = false;
+  }
+  // The elements of at least `bar` of one vector per lane, whose first element is e0.
+  template <typename T>
+  __device__ __forceinline__ void add(const uint4 &w, bool in, uint32_t e0) {
+    constexpr int N = Vec<T>::N;
+    if (!__any_sync(0xffffffffu, in && Vec<T>::max(w) >= bar)) return;
+    float v[N];
+    uint32_t want = 0;
+    Vec<T>::unpack(w, v);
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      if ((want >> j & 1) && key_of(v[j], e0 + j) <= full) want &= ~(1u << j);
-  }
-  lanes = __ballot_sync(0xffffffffu, want != 0);
-  while (lanes) {
-    const int src = __ffs(lanes) - 1;
-    uint64_t mine = 0;
-    if (lane == src) {
-      const int j = __ffs(want) - 1;
-      float f = v[0];
+      if (in && v[j] >= bar && v[j] > -INFINITY) want |= 1u << j;
+    uint32_t lanes = __ballot_sync(0xffffffffu, want != 0);
+    while (lanes) {
+      if (want) {
+        const int j = __ffs(want) - 1;
+        float f = v[0];
 #pragma unroll
-      for (int q = 1; q < N; ++q) f = q == j ? v[q] : f;
-      mine = key_of(f, e0 + j);
-      want &= want - 1;
+        for (int q = 1; q < N; ++q) f = q == j ? v[q] : f;
+        queue[waiting + __popc(lanes & ((1u << lane) - 1u))] = key_of(f, e0 + j);
+        want &= want - 1;
+      }
+      waiting += __popc(lanes);
+      if (waiting >= 32) {
+        merge(32);
+        __syncwarp();
+        const uint64_t rest = queue[32 + lane];
+        __syncwarp();
+        waiting -= 32;
+        if (lane < waiting) queue[lane] = rest;
+        // of equal values only those that still enter the list
+        const uint64_t last = __shfl_sync(0xffffffffu, list, top - 1);
+        if (last != 0) {
+          bar = ord_value(static_cast<uint32_t>(last >> 32));
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if ((want >> j & 1) && key_of(v[j], e0 + j) < last) want &= ~(1u << j);
+        }
+      }
+      lanes = __ballot_sync(0xffffffffu, want != 0);
     }
-    const uint64_t nk = __shfl_sync(0xffffffffu, mine, src);
-    const int pos = __popc(__ballot_sync(0xffffffffu, list > nk));
-    const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
-    if (lane >= pos) list = lane == pos ? nk : up;
-    lanes = __ballot_sync(0xffffffffu, want != 0);
   }
-}
+  __device__ __forceinline__ uint64_t finish() {
+    if (waiting) merge(waiting);
+    return list;
+  }
+};
 
 // The elements of at least `bar` of this warp's threads, as one descending list
-// of 32 over the lanes.  first: the first vector of lane 0.
-template <typename T>
-__device__ __forceinline__ uint64_t select_top(const Row<T> &r, int first, int stride, const Best &best, float bar, int lane) {
-  static_assert(kBatch == 8, "a batch of four threads to a warp");
-  uint64_t list = 0;
+// of 32 over the lanes, the first `top` of which are right.  first: the first
+// vector of lane 0.
+template <typename T, int B>
+__device__ __forceinline__ uint64_t select_top(const Row<T> &r, int first, int stride, const Best &best, float bar,
+                                               int top, uint64_t *queue, int lane) {
+  constexpr int OWNERS = 32 / B;
+  Select sel{queue, 0, bar, top, lane, 0, true};
   const bool mine = best.first >= bar && best.first > -INFINITY;
   uint32_t all = __ballot_sync(0xffffffffu, mine && best.second >= bar);
   uint32_t one = __ballot_sync(0xffffffffu, mine) & ~all;
-  // threads of which one batch reaches the bar, four at a time
+  // threads of which one batch reaches the bar: each its own, where that takes
+  // fewer steps (short rows), else OWNERS of them at a time
+  const int steps = min(B, (r.vecs + stride - 1) / stride);
+  if (steps * OWNERS < __popc(one) + OWNERS) {
+    const bool in1 = one >> lane & 1u;
+    one = 0;
+    for (int i = 0; i < steps; ++i) {
+      const long long u = best.batch + static_cast<long long>(i) * stride;
+      const bool in = in1 && u < r.vecs;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (in) w = r.load(static_cast<int>(u));
+      sel.add<T>(w, in, static_cast<uint32_t>(r.first(static_cast<int>(u))));
+    }
+  }
   while (one) {
     int owner = 32;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (lane >> 3 == i && one) owner = __ffs(one) - 1;
+    for (int i = 0; i < OWNERS; ++i) {
+      if (lane / B == i && one) owner = __ffs(one) - 1;
       one &= one - 1;
     }
     const int batch = __shfl_sync(0xffffffffu, best.batch, owner & 31);
-    const long long u = batch + static_cast<long long>(lane & 7) * stride;
+    const long long u = batch + static_cast<long long>(lane % B) * stride;
     const bool in = owner < 32 && u < r.vecs;
     uint4 w = make_uint4(0, 0, 0, 0);
     if (in) w = r.load(static_cast<int>(u));
-    insert_top<T>(w, in, static_cast<uint32_t>(r.first(static_cast<int>(u))), bar, list, lane);
+    sel.add<T>(w, in, static_cast<uint32_t>(r.first(static_cast<int>(u))));
   }
   // threads of which several do
   while (all) {
@@ -440,10 +501,10 @@ __device__ __forceinline__ uint64_t select_top(const Row<T> &r, int first, int s
       const bool in = u < r.vecs;
       uint4 w = make_uint4(0, 0, 0, 0);
       if (in) w = r.load(static_cast<int>(u));
-      insert_top<T>(w, in, static_cast<uint32_t>(r.first(static_cast<int>(u))), bar, list, lane);
+      sel.add<T>(w, in, static_cast<uint32_t>(r.first(static_cast<int>(u))));
     }
   }
-  return list;
+  return sel.finish();
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
@@ -462,11 +523,11 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t a) {
   return v;
 }
 
-// W warps to a row: one (four rows a block), or all of a block's; or, with
+// B 16-byte vectors are loaded at once.  W warps to a row: one (four rows a block), or all of a block's; or, with
 // CLUSTER, a cluster of a.blocks blocks, block `rank` taking the vectors u with
 // u / (32 W) % blocks == rank.
-template <typename T, bool TOP, int W, bool CLUSTER>
-__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? 8 : 32 / W) token_logprobs(const LpArgs a) {
+template <typename T, bool TOP, int W, int B, bool CLUSTER>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? (B == 4 ? 10 : 8) : 32 / W) token_logprobs(const LpArgs a) {
   constexpr int N = Vec<T>::N;
   static_assert(!CLUSTER || W == 8, "clusters are made of blocks of eight warps");
   __shared__ float sm[3][W];
@@ -475,6 +536,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? 8 : 32 / W) to
   __shared__ uint32_t maxima[TOP && W > 1 ? W : 1][32];
   __shared__ uint32_t s_best[TOP ? 32 : 1];
   __shared__ uint64_t s_top[TOP && CLUSTER ? 32 : 1];
+  __shared__ uint64_t queues[TOP ? (W == 1 ? 4 : W) : 1][64];
   const int warp = W == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = CLUSTER ? a.blocks : 1, rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
   const long long row = W == 1 ? blockIdx.x * 4ll + (threadIdx.x >> 5) : blockIdx.x / C;
@@ -489,24 +551,27 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? 8 : 32 / W) to
   {
     float2 s2 = make_float2(0.f, 0.f), t2 = s2;
     const int whole_end = static_cast<int>((static_cast<long long>(a.V) + r.shift) / N);
-    int u = rank * 32 * W + warp * 32 + lane;
-    if (r.shift == 0 || u > 0) {
-      const uint4 *src = reinterpret_cast<const uint4 *>(r.p - r.shift);  // vector 0, of which 0 .. shift - 1 is not ours
-      for (; u + (kBatch - 1) * stride < whole_end; u += kBatch * stride) {
-        uint4 w[kBatch];
+    const uint4 *src = reinterpret_cast<const uint4 *>(r.p - r.shift);  // vector 0, of which 0 .. shift - 1 is not ours
+    // u0: vector of lane 0; the same branches for the whole warp
+    for (int u0 = rank * 32 * W + warp * 32;;) {
+      const int u = u0 + lane;
+      uint4 w[B];
+      if ((r.shift == 0 || u0 > 0) && u0 + 31 + (B - 1) * stride < whole_end) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) w[i] = __ldg(src + u + i * stride);
-        add_batch<T, TOP>(w, u, st, s2, t2, best);
-      }
-    }
-    for (; u < r.vecs; u += kBatch * stride) {
-      uint4 w[kBatch];
+        for (int i = 0; i < B; ++i) w[i] = __ldg(src + u + i * stride);
+        add_batch<T, TOP, false>(w, u, B, st, s2, t2, best);
+      } else if (u0 < r.vecs) {
+        const int n = min(B, (r.vecs - u0 + stride - 1) / stride);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        w[i] = make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf);
-        if (u + i * stride < r.vecs) w[i] = r.load(u + i * stride);
+        for (int i = 0; i < B; ++i) {
+          w[i] = make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf);
+          if (i < n && u + i * stride < r.vecs) w[i] = r.load(u + i * stride);
+        }
+        add_batch<T, TOP, true>(w, u, n, st, s2, t2, best);
+      } else {
+        break;
       }
-      add_batch<T, TOP>(w, u, st, s2, t2, best);
+      u0 += B * stride;
     }
     st.s = s2.x + s2.y;
     st.t = t2.x + t2.y;
@@ -514,7 +579,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? 8 : 32 / W) to
   const float x_id = writer ? given_logit(a, r, id) : 0.f;  // not needed before the sums are joined
   uint32_t sorted = 0;
   if constexpr (TOP) {
-    sorted = warp_sort(ord_of(best.first), lane);
+    sorted = warp_largest(ord_of(best.first), a.top, lane);
     if (W > 1) maxima[warp][lane] = sorted;
   }
   Stat all = row_stats<W>(st, sm, warp, lane);
@@ -565,7 +630,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? 8 : 32 / W) to
   const RowResult res(all);
   if (writer) write_row(a, row, res, id, x_id);
   if constexpr (TOP) {
-    uint64_t key = select_top(r, rank * 32 * W + warp * 32, stride, best, bar, lane);
+    uint64_t key = select_top<T, B>(r, rank * 32 * W + warp * 32, stride, best, bar, a.top, queues[W == 1 ? threadIdx.x >> 5 : warp], lane);
     if constexpr (W > 1) {
       lists[warp][lane] = key;
       __syncthreads();
@@ -599,15 +664,17 @@ avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
   a.rows = rows;
   a.blocks = 1;
   // Few rows: several blocks a row, as long as a thread has four vectors and the
-  // blocks find room at once (1 x 50368 fp32: 9.8 us with one, 6.8 with eight;
-  // 300 rows: 14.8 with one, 20.6 with two).  Many rows: fewer warps to a row,
-  // whose ends cost less (6554 x 50368 bf16: 115 us with eight, 107 with four;
-  // 2000 x 2000: 10.4 with eight, 5.9 with four, 4.8 with one), unless a long
-  // row would be left to one warp at the end.
+  // blocks find room at once (1 x 50368 fp32: 6.2 us with one, 4.0 with eight;
+  // 300 rows: 14.0 with one, 18.5 with two).  Many rows: fewer warps to a row,
+  // whose ends cost less (6554 x 50368 bf16: 107 us with eight, 101 with four;
+  // 2000 x 2000: 9.8 with eight, 5.9 with four, 4.2 with one), unless a long
+  // row would be left to one warp at the end (5000 x 12000 fp32: 38 with four, 46
+  // with one; 18000 x 16000 bf16, 8 alternatives: 147 and 128).
   while (a.blocks < 8 && static_cast<long long>(rows) * a.blocks * 2 <= 2ll * sms && vecs >= 1024ll * a.blocks)
     a.blocks *= 2;
   const int C = a.blocks;
-  const int W = rows >= 8 * sms && vecs <= 1024 ? 1 : rows > 4 * sms || vecs <= 256 ? 4 : 8;
+  const bool narrow = rows >= 8 * sms && vecs <= (rows >= 48 * sms ? 2048 : 1024);
+  const int W = narrow ? 1 : rows > 4 * sms || vecs <= 256 ? 4 : 8;
   cudaLaunchConfig_t cfg{};
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -621,10 +688,14 @@ avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
   }
   cfg.gridDim = dim3(W == 1 && C == 1 ? (static_cast<unsigned>(rows) + 3) / 4 : static_cast<unsigned>(rows) * C);
   cfg.blockDim = dim3(C > 1 || W == 8 ? 256 : 128);
-  const cudaError_t e = C > 1    ? cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, 8, true>, static_cast<const LpArgs>(a))
-                        : W == 1 ? cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, 1, false>, static_cast<const LpArgs>(a))
-                        : W == 4 ? cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, 4, false>, static_cast<const LpArgs>(a))
-                                 : cudaLaunchKernelEx(&cfg, token_logprobs<T, TOP, 8, false>, static_cast<const LpArgs>(a));
+  // rows of at most four vectors a lane: batches of four, more warps an SM
+  // (30000 x 250 bf16: 18.2 us with batches of eight, 14.9 with four)
+  void (*const kern)(LpArgs) = C > 1                ? token_logprobs<T, TOP, 8, 8, true>
+                               : W == 1 && vecs <= 128 ? token_logprobs<T, TOP, 1, 4, false>
+                               : W == 1                ? token_logprobs<T, TOP, 1, 8, false>
+                               : W == 4                ? token_logprobs<T, TOP, 4, 8, false>
+                                                       : token_logprobs<T, TOP, 8, 8, false>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess) {
     cudaGetLastError();
     set_detail("token_logprobs launch failed: %s", cudaGetErrorString(e));
@@ -639,7 +710,7 @@ avey_status run_logprobs(LpArgs a, int rows, cudaStream_t s) {
 struct LpGradArgs {
   const void *x;
   long long ld;
-  int V, parts;  // blocks of a row
+  int rows, V, parts;  // blocks of a row
   const int32_t *ids;
   const float *stats, *entropy, *d_logprob, *d_entropy;
   void *dx;
@@ -650,18 +721,23 @@ struct LpGradArgs {
 constexpr int kGradBatch = 4;  // vectors a thread loads at once
 constexpr int kGradVecs = 8;   // and takes at most
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_grad(const LpGradArgs a) {
+// TPR threads to a row's part: a whole block, or a warp to a whole row.
+template <typename T, int TPR>
+__global__ void __launch_bounds__(kLpThreads, TPR == 32 ? 5 : 0) token_logprobs_grad(const LpGradArgs a) {
   constexpr int N = Vec<T>::N;
-  const long long row = blockIdx.x / a.parts;
-  const int part = static_cast<int>(blockIdx.x - row * a.parts);
+  constexpr bool BLOCK = TPR == kLpThreads;
+  const long long row =
+      BLOCK ? blockIdx.x / a.parts : blockIdx.x * static_cast<long long>(kLpThreads / TPR) + threadIdx.x / TPR;
+  if (!BLOCK && row >= a.rows) return;
+  const int part = BLOCK ? static_cast<int>(blockIdx.x - row * a.parts) : 0;
+  const int me = threadIdx.x % TPR;
   const Row<T> r(static_cast<const T *>(a.x) + row * a.ld, a.V);
   T *out = static_cast<T *>(a.dx) + row * a.ld_d;
   // whole vectors of x are whole 16-byte words of the gradient too
   const bool same = ((reinterpret_cast<uintptr_t>(r.p) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
   int id = a.d_logprob ? a.ids[row] : -1;
   if (id >= a.V) {
-    if (part == 0 && threadIdx.x == 0) record_status(a.status, AVEY_ERR_DEVICE_BOUNDS);
+    if (part == 0 && me == 0) record_status(a.status, AVEY_ERR_DEVICE_BOUNDS);
     id = -1;
   }
   const float g = id >= 0 ? a.d_logprob[row] : 0.f;
@@ -697,31 +773,16 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_grad(const LpGradAr
   const int per = (r.vecs + a.parts - 1) / a.parts;
   const int begin = part * per, end = min(r.vecs, begin + per);
   const int hi = static_cast<int>((static_cast<long long>(a.V) + r.shift) / N);
-  int u = begin + static_cast<int>(threadIdx.x);
   const int fast_end = same && !none ? min(end, hi) : 0;
-  if (u > 0 || r.shift == 0) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(r.p - r.shift);
-    uint4 *dst = reinterpret_cast<uint4 *>(out - r.shift);
-    for (; u + (kGradBatch - 1) * kLpThreads < fast_end; u += kGradBatch * kLpThreads) {
-      uint4 w[kGradBatch];
-#pragma unroll
-      for (int i = 0; i < kGradBatch; ++i) w[i] = src[u + i * kLpThreads];
-#pragma unroll
-      for (int i = 0; i < kGradBatch; ++i) {
-        float v[N];
-        gradient(w[i], v, id - r.first(u + i * kLpThreads));
-        dst[u + i * kLpThreads] = Vec<T>::pack(v);
-      }
-    }
-  }
-  for (; u < end; u += kLpThreads) {
+  // Vector u, whose elements are w, some of which may not exist.
+  auto put = [&](int u, const uint4 &w) {
     const int e0 = r.first(u);
     float v[N];
     if (none) {
 #pragma unroll
       for (int j = 0; j < N; ++j) v[j] = 0.f;
     } else {
-      gradient(r.load(u), v, id >= 0 ? id - e0 : -1);
+      gradient(w, v, id >= 0 ? id - e0 : -1);
     }
     if (same && r.whole(u)) {
       *reinterpret_cast<uint4 *>(out + e0) = Vec<T>::pack(v);
@@ -730,16 +791,58 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_grad(const LpGradAr
       for (int j = 0; j < N; ++j)
         if (e0 + j >= 0 && e0 + j < a.V) out[e0 + j] = Vec<T>::from_f(v[j]);
     }
+  };
+  const uint4 *src = reinterpret_cast<const uint4 *>(r.p - r.shift);
+  uint4 *dst = reinterpret_cast<uint4 *>(out - r.shift);
+  int u = begin + me;
+  // The vector that begins before the row: a warp's lane goes on in step with the
+  // others; in a block its thread takes its few vectors one by one.
+  const bool apart = u == 0 && r.shift != 0;
+  if (!BLOCK && apart) {
+    put(0, r.load(0));
+    u = TPR;
+  }
+  for (; (!BLOCK || !apart) && u + (kGradBatch - 1) * TPR < fast_end; u += kGradBatch * TPR) {
+    uint4 w[kGradBatch];
+#pragma unroll
+    for (int i = 0; i < kGradBatch; ++i) w[i] = src[u + i * TPR];
+#pragma unroll
+    for (int i = 0; i < kGradBatch; ++i) {
+      float v[N];
+      gradient(w[i], v, id - r.first(u + i * TPR));
+      dst[u + i * TPR] = Vec<T>::pack(v);
+    }
+  }
+  if constexpr (BLOCK) {
+    for (; u < end; u += TPR) put(u, none ? make_uint4(0, 0, 0, 0) : r.load(u));
+  } else {
+    for (; u < end; u += kGradBatch * TPR) {
+      uint4 w[kGradBatch];
+#pragma unroll
+      for (int i = 0; i < kGradBatch; ++i)
+        if (u + i * TPR < end) w[i] = r.load(u + i * TPR);
+#pragma unroll
+      for (int i = 0; i < kGradBatch; ++i)
+        if (u + i * TPR < end) put(u + i * TPR, w[i]);
+    }
   }
 }
 
 template <typename T>
 avey_status run_logprobs_grad(LpGradArgs a, int rows, cudaStream_t s) {
   const long long vecs = (static_cast<long long>(a.V) + 2 * Vec<T>::N - 2) / Vec<T>::N;
+  // Short rows: a warp to each (30000 x 1000 bf16: 63 us with a block, 28 so; 8000 x
+  // 4096: 31 and 22; 3000 x 8192: 16.0 and 17.0).
+  if (vecs <= 1024 && rows >= 8 * sm_count()) {
+    a.parts = 1;
+    token_logprobs_grad<T, 32><<<(static_cast<unsigned>(rows) + 7) / 8, kLpThreads, 0, s>>>(a);
+    AVEY_CHECK_LAUNCH("token_logprobs_grad", s);
+    return AVEY_OK;
+  }
   long long parts = (vecs + kGradVecs * kLpThreads - 1) / (kGradVecs * kLpThreads);
   parts = std::max<long long>(1, std::min<long long>(parts, 0x7fffffffll / rows));
   a.parts = static_cast<int>(parts);
-  token_logprobs_grad<T><<<static_cast<unsigned>(rows * parts), kLpThreads, 0, s>>>(a);
+  token_logprobs_grad<T, kLpThreads><<<static_cast<unsigned>(rows * parts), kLpThreads, 0, s>>>(a);
   AVEY_CHECK_LAUNCH("token_logprobs_grad", s);
   return AVEY_OK;
 }
@@ -839,6 +942,7 @@ extern "C" avey_status avey_token_logprobs_backward(const void *logits, avey_dty
   LpGradArgs a{};
   a.x = logits;
   a.ld = ld;
+  a.rows = rows;
   a.V = V;
   a.ids = ids;
   a.stats = stats;

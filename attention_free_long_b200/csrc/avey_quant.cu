@@ -91,7 +91,7 @@ template <int DT, bool PRENORM, bool FAST>
 avey_status run_quantize(const void *x, int rows, int cols, long long ld_x, int8_t *q, long long ld_q,
                          float *scale, cudaStream_t s) {
 #define AVEY_QUANTIZE(LPR) \
-  quantize_rows<DT, LPR, PRENORM, FAST><<<(rows + 256 / LPR - 1) / (256 / LPR), 256, 0, s>>>(x, rows, cols, ld_x, q, ld_q, scale)
+  quantize_rows<DT, LPR, PRENORM, FAST><<<(rows - 1) / (256 / LPR) + 1, 256, 0, s>>>(x, rows, cols, ld_x, q, ld_q, scale)
   // a thread holds 32 values; with fewer rows than SMs a block per row spreads
   // the loads of a row
   if (cols > 128 * 32 || (rows <= sm_count() && cols > 256))
@@ -160,6 +160,12 @@ extern "C" avey_status avey_quantize_rows(const void *x, avey_dtype dt, int rows
   AVEY_REQUIRE(x && q && scale, AVEY_ERR_INVALID_ARG, "avey_quantize_rows: null pointer");
   AVEY_REQUIRE(aligned16(q) && (reinterpret_cast<uintptr_t>(scale) & 3) == 0, AVEY_ERR_INVALID_ARG,
                "avey_quantize_rows: q 16-byte and scale 4-byte aligned");
+  {
+    const uintptr_t n = static_cast<uintptr_t>(rows - 1), es = dt == AVEY_F32 ? 4 : 2;
+    const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), q0 = reinterpret_cast<uintptr_t>(q);
+    const uintptr_t xn = x0 + (n * ld_x + cols + (dt == AVEY_BF16X2 ? rows * ld_x : 0)) * es;
+    AVEY_REQUIRE(xn <= q0 || q0 + n * ld_q + cols <= x0, AVEY_ERR_INVALID_ARG, "avey_quantize_rows: q overlaps x");
+  }
   return launch_quantize_rows(x, dt, rows, cols, ld_x, prenorm ? 1 : 0, q, ld_q, scale,
                               reinterpret_cast<cudaStream_t>(stream));
 }

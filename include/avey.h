@@ -369,7 +369,7 @@ AVEY_API size_t avey_layer_workspace_bytes_ex(avey_dtype dt, int T, int d, int m
  *        behind are left as they were.  16-byte aligned, ld_q % 16 == 0.
  * scale  [rows] fp32 out.
  * Constraints: rows >= 0 (0: nothing is done), cols >= 1, ld_x >= cols,
- * ld_q >= cols.
+ * ld_q >= cols; q must not overlap x (checked).
  */
 AVEY_API avey_status avey_quantize_rows(const void *x, avey_dtype dt, int rows, int cols,
                                         int64_t ld_x, int prenorm, int8_t *q, int64_t ld_q,

@@ -336,3 +336,77 @@ def test_binding_refuses(cuda_dev):
         av.avey_token_logprobs_backward(t, None, r, torch.ones(4, device=cuda_dev))
     with pytest.raises(TypeError):
         av.avey_token_logprobs_backward(t, ids, r, torch.ones(4, device=cuda_dev), out=t.bfloat16())
+
+
+def _orders(rows, V, kind, dtype, dev):
+    """Rows whose alternatives reach the selection in a hard order."""
+    rng = np.random.default_rng(V)
+    if kind == "ascending":
+        x = np.sort(rng.standard_normal((rows, V)) * 3, axis=1)
+    elif kind == "descending":
+        x = -np.sort(rng.standard_normal((rows, V)) * 3, axis=1)
+    elif kind == "constant":
+        x = np.repeat(rng.standard_normal((rows, 1)), V, axis=1)
+    else:  # "few": many equal values, the largest at the end
+        x = rng.integers(-3, 3, (rows, V)).astype(np.float64)
+        x[:, V - 1 - rng.integers(0, min(V, 40), rows)] = 4.0
+    t = torch.from_numpy(x.astype(np.float32)).to(dev, dtype)
+    return t, t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["ascending", "descending", "constant", "few"])
+@pytest.mark.parametrize("rows,V", [
+    (1190, 70), (1190, 512), (1190, 1025), (1190, 4090), (2, 700), (200, 6000), (700, 5000), (3, 40000)])
+def test_alternatives_in_hard_orders(rows, V, kind, dtype, cuda_dev):
+    t, x = _orders(rows, V, kind, dtype, cuda_dev)
+    ids, dids = _ids(rows, V, V, cuda_dev)
+    for top in (1, 4, 5, 32):
+        _check(t, x, ids, top, av.avey_token_logprobs(t, dids, top=top))
+
+
+def test_a_warp_to_each_of_many_rows(cuda_dev):
+    rows, V = 7200, 4101
+    t, x = _orders(rows, V, "few", torch.float32, cuda_dev)
+    ids, dids = _ids(rows, V, V, cuda_dev)
+    _check(t, x, ids, 7, av.avey_token_logprobs(t, dids, top=7))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,offset,pad", [(1, 0, 0), (5, 1, 2), (100, 3, 1), (517, 1, 0), (1000, 0, 8), (4085, 7, 3)])
+def test_many_short_rows_anywhere(V, offset, pad, dtype, cuda_dev):
+    rows = 1301
+    t, x = _logits(rows, V, dtype, V, cuda_dev, masked=0.2 if V > 50 else 0.0)
+    ids, dids = _ids(rows, V, 3, cuda_dev)
+    wide = torch.full((rows * (V + pad) + offset + 16,), float("inf"), dtype=dtype, device=cuda_dev)
+    view = wide[offset:offset + rows * (V + pad)].view(rows, V + pad)[:, :V]
+    view.copy_(t)
+    r = av.avey_token_logprobs(view, dids, top=8)
+    _check(view, x, ids, 8, r)
+    g, h = torch.randn(rows, device=cuda_dev), torch.randn(rows, device=cuda_dev)
+    g[::7], h[::7] = 0, 0
+    dense = av.avey_token_logprobs_backward(t, dids, r, g, h)
+    want = torch.zeros(rows, V, dtype=torch.float64, device=cuda_dev)
+    m, z = r.stats[:, 0].double(), r.stats[:, 1].double()
+    lp = torch.clamp(t.double() - m[:, None] - z[:, None], min=-200)
+    p = lp.exp()
+    gg = torch.where(dids >= 0, g, 0).double()
+    want = -p * (gg[:, None] + h.double()[:, None] * (lp + r.entropy.double()[:, None]))
+    want[torch.arange(rows), dids.clamp(min=0).long()] += gg
+    # p: its exponent has 3 roundings of |lp|, the unit 4u, the bracket 4 roundings
+    # of the sum of its terms, the last addition and the output one each
+    size = gg.abs()[:, None] + h.double().abs()[:, None] * (lp.abs() + r.entropy.double()[:, None])
+    tol = U * (3 * lp.abs() + 12) * p * size + (HALF[dtype] + 2 * U) * want.abs() + 1e-37
+    assert bool(((dense.double() - want).abs() <= tol).all())
+    assert bool((dense[::7] == 0).all())
+    for off2 in (offset, offset + 1):
+        buf = torch.full((rows * (V + pad) + off2 + 16,), 5.0, dtype=dtype, device=cuda_dev)
+        out = buf[off2:off2 + rows * (V + pad)].view(rows, V + pad)
+        av.avey_token_logprobs_backward(view, dids, r, g, h, out=out[:, :V])
+        assert torch.equal(out[:, :V], dense)
+        assert bool((out[:, V:] == 5).all()) and bool((buf[:off2] == 5).all())
+        assert bool((buf[off2 + rows * (V + pad):] == 5).all())
+    av.avey_token_logprobs_backward(view, dids, r, g, h, out=view)  # in place
+    assert torch.equal(view, dense)
+    rest = wide[offset:offset + rows * (V + pad)].view(rows, V + pad)[:, V:]
+    assert bool(torch.isinf(rest).all()) and bool(torch.isinf(wide[:offset]).all())

@@ -30,6 +30,8 @@ def _quantize(**kw):
     (dict(ld_q=40), 1, "ld_q"), (dict(ld_q=32), 1, "ld_q"), (dict(dt=av.AVEY_I8), 2, "dtype"),
     (dict(x=A + 2), 1, "aligned"), (dict(q=A + 8), 1, "aligned"), (dict(scale=A + 2), 1, "aligned"),
     (dict(cols=(1 << 30) + 1, ld=1 << 31, ld_q=1 << 31), 2, "2^30"),
+    (dict(), 1, "overlaps"), (dict(q=A + 512), 1, "overlaps"), (dict(q=A - 176), 1, "overlaps"),
+    (dict(dt=av.AVEY_BF16X2, q=A + 624), 1, "overlaps"),
 ])
 def test_quantize_rows_refuses(kw, code, word):
     _refused(_quantize(**kw), code, word)
