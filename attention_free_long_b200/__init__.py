@@ -447,8 +447,8 @@ def avey_quantize_rows(x: torch.Tensor, prenorm: bool = False) -> QuantRows:
     [2, rows, cols]) as 8-bit integers with a scale per row; prenorm: of the
     RMS-normalised rows."""
     dt, rows, cols, ld = _quant_source(x)
-    q = x.new_empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8)
-    scale = x.new_empty((rows,), dtype=torch.float32)
+    q = x.new_empty(rows, (cols + 15) // 16 * 16, dtype=torch.int8)
+    scale = x.new_empty(rows, dtype=torch.float32)
     _call("avey_quantize_rows", x, x.data_ptr(), dt, rows, cols, ld, 1 if prenorm else 0, q.data_ptr(),
           q.shape[1], scale.data_ptr())
     return QuantRows(q, scale, cols)
@@ -482,7 +482,7 @@ def _scratch(ws: Optional[torch.Tensor], need: int, t: torch.Tensor):
     if need == 0:
         return None, 0
     if ws is None or ws.numel() < need:
-        ws = t.new_empty((need,), dtype=torch.uint8)
+        ws = t.new_empty(need, dtype=torch.uint8)
     elif not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous()):
         raise ValueError("ws must be a contiguous CUDA uint8 tensor")
     return ws, ws.numel()
@@ -507,9 +507,9 @@ def avey_linear_i8(x, lin: QuantLinear, act: int = AVEY_ACT_NONE,
     if out is None:
         ld_out = (N + 7) // 8 * 8
         if pair:
-            out = t.new_empty((2, rows, ld_out), dtype=torch.bfloat16)
+            out = t.new_empty(2, rows, ld_out, dtype=torch.bfloat16)
         else:
-            out = t.new_empty((rows, ld_out), dtype=out_dtype)
+            out = t.new_empty(rows, ld_out, dtype=out_dtype)
         if ld_out != N:
             out = out[..., :N]
     elif pair:
@@ -549,7 +549,7 @@ class TokenLogprobs:
 
 def _score_outputs(t: torch.Tensor, rows: int, given: bool, top: int) -> TokenLogprobs:
     """The outputs of one call, in one allocation on t's device."""
-    buf = t.new_empty(((4 if given else 3) * rows + 2 * top * rows,), dtype=torch.float32)
+    buf = t.new_empty((4 if given else 3) * rows + 2 * top * rows, dtype=torch.float32)
     row = (1,)
     r = TokenLogprobs(None, buf.as_strided((rows, 2), (2, 1), 0), buf.as_strided((rows,), row, 2 * rows))
     at = 3 * rows
@@ -597,7 +597,7 @@ def avey_token_logprobs_backward(logits: torch.Tensor, ids: Optional[torch.Tenso
     if scores.stats.dtype != torch.float32 or scores.stats.shape != (rows, 2):
         raise TypeError(f"stats must be fp32 [{rows}, 2]")
     if out is None:
-        out, ld_d = logits.new_empty((rows, V)), V
+        out, ld_d = logits.new_empty(rows, V), V
     else:
         r, c, ld_d = _rows_of(out, "out")
         if (r, c) != (rows, V) or out.dtype != logits.dtype:
