@@ -10,9 +10,10 @@
 // 64-byte pieces of 16 rows; rows are prefetched into L2 before the block
 // prepares its tokens.  Rows that come unrounded are quantised by every block for
 // itself (a few KB from L2), which saves the launch of the rounding kernel.
-// 16 rows of 8-bit integers against 50368 x 768 weights take 10.1 us here and
-// 16.1 us as a tile of 256; from 17 rows on the tile wins (20 rows against
-// 1536 x 768: 9.8 and 6.3 us), since more rows mean more to prepare per block.
+// 12 rows against 50368 x 768 weights take 13.1 us here; rounded apart and with
+// channels as the rows of a tile 13.5, two launches.  More rows or longer ones mean
+// more to prepare per block: from 9 rows on only up to K = 768 (12 rows against
+// 65536 x 1024: 19.4 and 17.4 us; 40000 x 2048: 27.5 and 21.7), and none from 17.
 #include <algorithm>
 
 #include "avey_common.cuh"
@@ -86,8 +87,11 @@ __device__ __forceinline__ void quantize_row_to(const FewArgs &a, int row, int8_
 }
 
 // NB blocks of eight tokens, WARPS x 16 channels a block, DT the type of x.
+// Two blocks of tokens: four thread blocks an SM, or from 56832 channels on some
+// wait and prepare the tokens after the others (12 x 768 -> 65536: 19.9 us with three
+// an SM, 15.7 with four; 50368: 12.9 and 13.4).
 template <int NB, int WARPS, int DT, int OUT>
-__global__ void __launch_bounds__(WARPS * 32) linear_i8_few(const FewArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, NB == 2 && WARPS == 8 ? 4 : 0) linear_i8_few(const FewArgs a) {
   extern __shared__ __align__(16) int8_t xs_q[];
   __shared__ float xs[NB * 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -234,7 +238,7 @@ inline int few_blocks(int rows) { return rows <= 8 ? 1 : 2; }
 }  // namespace
 
 bool linear_few_fits(int rows, int K) {
-  return rows <= kFewRows && static_cast<long long>(few_blocks(rows)) * 8 * few_stride(K) <= kFewShared;
+  return rows <= kFewRows && (few_blocks(rows) == 1 || K <= 768) && K <= kFewShared && 8 * few_stride(K) <= kFewShared;
 }
 
 bool linear_few_quantizes(avey_dtype x_dt, int rows, int K) {

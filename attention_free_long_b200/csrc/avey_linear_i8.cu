@@ -15,6 +15,7 @@
 // from L2 and into shared memory, 44 instead of 48 us for 8192 x 768 x 8192 to
 // bf16.
 #include <algorithm>
+#include <utility>
 
 #include "avey_common.cuh"
 #include "avey_internal.h"
@@ -54,12 +55,13 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // AVEY_BF16X2 (stores): running softmax statistics of each row.
 constexpr int kScore = -1;
 
-template <int BN, int OUT, bool RES, bool ARES>
+template <int BN, int OUT, bool RES, bool ARES, bool SWAP = false>
 struct LinLayout {
   static constexpr int PM = 256;
   // epilogue warps: sixteen, but for fp32 outputs (8192 x 768 x 8192: 63 us with
-  // eight, 69 with sixteen; 32768 x 768 x 1536 to pairs: 62 and 55)
-  static constexpr int EPI = OUT == AVEY_F32 ? 8 : 16;
+  // eight, 69 with sixteen; 32768 x 768 x 1536 to pairs: 62 and 55) and for the two
+  // chunks of a quarter's rows that swapped tiles have
+  static constexpr int EPI = OUT == AVEY_F32 || SWAP ? 8 : 16;
   static constexpr int GROUPS = EPI / 4;                // warps that share a quarter's chunks
   static constexpr int THREADS = 64 + 32 * EPI;
   static constexpr uint32_t A_BYTES = 128 * kBK;        // this CTA's rows, one K step
@@ -67,7 +69,7 @@ struct LinLayout {
   static constexpr uint32_t STAGE_BYTES = ARES ? B_BYTES : A_BYTES + B_BYTES;
   // staging of stores (and of the residual, fetched a chunk ahead): a 32 x 32
   // chunk a buffer
-  static constexpr uint32_t BUF = OUT == kScore ? 0 : OUT == AVEY_BF16 ? 2048 : 4096;
+  static constexpr uint32_t BUF = OUT == kScore || SWAP ? 0 : OUT == AVEY_BF16 ? 2048 : 4096;
   static constexpr int BUFS = RES ? 3 : 1;
   static constexpr uint32_t STAGING_BYTES = EPI * BUFS * BUF;
   static constexpr uint32_t CTRL_BYTES = 1024;
@@ -226,6 +228,51 @@ __device__ __forceinline__ void lin_values(float (&v)[32], float xs, const float
   }
 }
 
+// The same with channels as rows (this lane's scale ws and bias bs) and tokens as
+// columns, whose scales are w.
+__device__ __forceinline__ void lin_values_swapped(float (&v)[32], float ws, float bs, const float *x, int relu2) {
+  const float2 w2 = make_float2(ws, ws), b2 = make_float2(bs, bs);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float4 x4 = *reinterpret_cast<const float4 *>(x + 4 * q);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 f = make_float2(static_cast<float>(__float_as_int(v[4 * q + 2 * h])),
+                                   static_cast<float>(__float_as_int(v[4 * q + 2 * h + 1])));
+      float2 y = ffma2(fmul2(f, h ? make_float2(x4.z, x4.w) : make_float2(x4.x, x4.y)), w2, b2);
+      if (relu2) {
+        y = make_float2(max_nan(y.x, 0.f), max_nan(y.y, 0.f));  // NaN stays NaN
+        y = fmul2(y, y);
+      }
+      v[4 * q + 2 * h] = y.x;
+      v[4 * q + 2 * h + 1] = y.y;
+    }
+  }
+}
+
+// A 32 x 32 chunk of channels x tokens: each token's 32 channels are one store.
+template <int OUT>
+__device__ __forceinline__ void store_swapped(const LinArgs &a, int channel, int token0, const float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const long long t = token0 + j;
+    if (t >= a.N) break;
+    float y = v[j];
+    if constexpr (OUT == AVEY_F32) {
+      if (a.residual) y += a.residual[t * a.ld_res + channel];
+      static_cast<float *>(a.out)[t * a.ld_out + channel] = y;
+    } else {
+      bf16 *hi = static_cast<bf16 *>(a.out) + t * a.ld_out + channel;
+      *hi = __float2bfloat16_rn(y);
+      if constexpr (OUT == AVEY_BF16X2) {
+        float h, l;
+        split_bf16(y, h, l);
+        hi[a.N * a.ld_out] = __float2bfloat16_rn(l);
+      }
+    }
+  }
+}
+
 // A 32-column chunk into a row's running statistics.
 __device__ __forceinline__ void score_values(float (&v)[32], float xs, const float *w, const float *b,
                                              Stat2 &st) {
@@ -260,12 +307,15 @@ __device__ __forceinline__ void score_values(float (&v)[32], float xs, const flo
   st.t += t[0].x + t[0].y;
 }
 
-template <int BN, int OUT, bool RES, bool ARES>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, RES, ARES>::THREADS, 1)
+// SWAP: few tokens against many channels.  The channels are the rows (A), the
+// tokens the columns, so that all lanes of TMEM and all epilogue warps have work;
+// LinArgs' rows counts channels and N tokens, and outputs go straight to memory.
+template <int BN, int OUT, bool RES, bool ARES, bool SWAP = false>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, RES, ARES, SWAP>::THREADS, 1)
     linear_i8_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
                    const __grid_constant__ CUtensorMap tmR, const LinArgs a) {
-  using P = LinLayout<BN, OUT, RES, ARES>;
+  using P = LinLayout<BN, OUT, RES, ARES, SWAP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
@@ -327,8 +377,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
-    if (OUT != kScore) prefetch_tmap(&tmO0);
-    if (OUT == AVEY_BF16X2) prefetch_tmap(&tmO1);
+    if (OUT != kScore && !SWAP) prefetch_tmap(&tmO0);
+    if (OUT == AVEY_BF16X2 && !SWAP) prefetch_tmap(&tmO1);
     if (RES) prefetch_tmap(&tmR);
   }
   cluster_sync_all();
@@ -481,7 +531,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
     auto row_of = [&](int mt) { return mt * P::PM + static_cast<int>(rank) * 128 + quarter * 32; };
     auto row_scale = [&](int mt) {
       const int row = row_of(mt) + lane;
-      return row < a.rows ? __ldg(a.x_scale + row) * (OUT == kScore ? kLog2e : 1.f) : 0.f;
+      return row < a.rows ? __ldg((SWAP ? a.w_scale : a.x_scale) + row) * (OUT == kScore ? kLog2e : 1.f) : 0.f;
+    };
+    auto row_bias = [&](int mt) {
+      const int row = row_of(mt) + lane;
+      return SWAP && a.bias && row < a.rows ? __ldg(a.bias + row) : 0.f;
     };
     // Scale and bias of this lane's column of CHUNKS chunks from column block nt,
     // chunk ch: fetched a chunk (scores: a tile) ahead, and nothing is computed
@@ -496,8 +550,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
         cw[i] = 0.f;
         cb[i] = OUT == kScore ? kMaskedWord : 0.f;
         if (c < a.N) {
-          cw[i] = __ldg(a.w_scale + c);
-          if (a.bias)
+          cw[i] = __ldg((SWAP ? a.x_scale : a.w_scale) + c);
+          if (!SWAP && a.bias)
             cb[i] = __ldg(a.bias + c);
           else if (OUT == kScore)
             cb[i] = 0.f;
@@ -527,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
     uint32_t acc_phase = 0, res_phase = 0;  // res_phase: a bit for each buffer
     bool ok = true, have = false;           // have: this chunk's columns and residual have been fetched
     TileWalk walk(a, t_first, t_end, t_step);
-    float xs_next = walk.more() ? row_scale(walk.mt) : 0.f;
+    float xs_next = walk.more() ? row_scale(walk.mt) : 0.f, bs_next = walk.more() ? row_bias(walk.mt) : 0.f;
     if (OUT == kScore && walk.more()) fetch_columns(walk.nt, group);
     Stat2 st{kLowest, 0.f, 0.f};
     while (walk.more()) {
@@ -536,8 +590,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
       const int row0 = row_of(mt);
       const int row = row0 + lane;
       const bool valid = row < a.rows;
-      const float xs = xs_next;
-      if (walk.more() && walk.mt != mt) xs_next = row_scale(walk.mt);
+      const float xs = xs_next, bs = bs_next;
+      if (walk.more() && walk.mt != mt) {
+        xs_next = row_scale(walk.mt);
+        bs_next = row_bias(walk.mt);
+      }
       if constexpr (OUT == kScore) {
         __syncwarp();  // the last tile's columns have been read
         put_columns();
@@ -577,6 +634,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
         tmem_ld32(taddr + ch * 32, v);
         if constexpr (OUT == kScore) {
           score_values(v, xs, w_s, b_s, st);
+        } else if constexpr (SWAP) {
+          lin_values_swapped(v, xs, bs, w_s, a.relu2);
+          __syncwarp();
+          if (valid) store_swapped<OUT>(a, row, col0, v);
         } else {
           lin_values(v, xs, w_s, b_s, a.relu2);
           __syncwarp();
@@ -666,7 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
             if (coming >> i & 1u) drain_wait(res_bar(ew, i), res_phase >> i & 1u);
       }
     }
-    if (OUT != kScore && lane == 0) bulk_wait_all();  // outputs written
+    if (OUT != kScore && !SWAP && lane == 0) bulk_wait_all();  // outputs written
   }
 
   tc_fence_before();
@@ -682,12 +743,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
   cluster_sync_all();
 }
 
-template <int BN, int OUT, bool RES, bool ARES>
+template <int BN, int OUT, bool RES, bool ARES, bool SWAP = false>
 avey_status run_linear_pair(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &o0,
                             const CUtensorMap &o1, const CUtensorMap &r, LinArgs a, int pairs, bool after,
                             cudaStream_t st) {
-  using P = LinLayout<BN, OUT, RES, ARES>;
-  auto kern = linear_i8_pair<BN, OUT, RES, ARES>;
+  using P = LinLayout<BN, OUT, RES, ARES, SWAP>;
+  auto kern = linear_i8_pair<BN, OUT, RES, ARES, SWAP>;
   const int ksteps = (a.K + kBK - 1) / kBK;
   a.stages = P::stages(ksteps);
   a.tiles_bytes = P::tiles_bytes(ksteps);
@@ -756,6 +817,28 @@ avey_status run_linear_bn(const avey_linear_i8_params *p, const int8_t *xq, int6
 #undef AVEY_LINEAR
 }
 
+constexpr int kSwapRows = 64;
+inline bool swap_pays(int rows, int N) { return rows <= kSwapRows && (N + 255ll) / 256 * 8 > sm_count(); }
+
+// Up to kSwapRows tokens against all channels, channels as rows.
+avey_status run_linear_swapped(const avey_linear_i8_params *p, const int8_t *xq, int64_t ld_xq, LinArgs a,
+                               void *out, avey_dtype out_dt, bool after, cudaStream_t s) {
+  CUtensorMap ma, mb;
+  if (!encode_i8_map(&ma, p->Wq, a.K, a.N, p->ld_w, 128)) return AVEY_ERR_CUDA;
+  if (!encode_i8_map(&mb, xq, a.K, a.rows, ld_xq, kSwapRows / 2)) return AVEY_ERR_CUDA;
+  std::swap(a.rows, a.N);
+  a.tiles_m = (a.rows + 255) / 256;
+  a.tiles_n = 1;
+  a.num_tiles = a.tiles_m;
+  a.out = out;
+  const int pairs = pairs_for(a.num_tiles);
+#define AVEY_LINEAR(OUT) run_linear_pair<kSwapRows, OUT, false, false, true>(ma, mb, ma, ma, ma, a, pairs, after, s)
+  if (out_dt == AVEY_BF16) return AVEY_LINEAR(AVEY_BF16);
+  if (out_dt == AVEY_BF16X2) return AVEY_LINEAR(AVEY_BF16X2);
+  return AVEY_LINEAR(AVEY_F32);
+#undef AVEY_LINEAR
+}
+
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 inline int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
@@ -779,11 +862,17 @@ avey_status launch_linear_i8(const avey_linear_i8_params *p, const int8_t *xq, i
   a.ld_res = ld_res;
   a.ld_out = ld_out;
   a.status = device_status_word();
+  // Up to 64 tokens against many channels: channels as rows (32 x 768 x 50368 to
+  // fp32: 17.3 us as a tile of 256 tokens, of which two of eight warps' lanes hold
+  // one, 13.0 so; 16384 channels 10.3 and 8.1, 4096 6.4 and 6.4, 1536 6.2 and 6.4;
+  // 128 tokens to bf16 15.6 and 17.0).
+  const long long tm = (rows + 255) / 256, pairs = sm_count() / 2;
+  if (swap_pays(rows, p->N))
+    return run_linear_swapped(p, xq, ld_xq, a, out, out_dt, after, s);
   // The widest tile that gives every pair of SMs one, 128 columns down to every
   // second pair (1003 x 1008 x 2048: 9.8 us with 64, 9.0 with 128, 11.2 with 256;
   // 256 x 256 x 256: 5.5, 6.4 and 8.2; 4096 x 768 x 1536: 16.4, 12.2 and 12.4;
   // 32768 x 768 x 1536: 64, 44 and 38).
-  const long long tm = (rows + 255) / 256, pairs = sm_count() / 2;
   if (tm * ((p->N + 255) / 256) >= pairs) return run_linear_bn<256>(p, xq, ld_xq, a, out, out_dt, after, s);
   if (2 * tm * ((p->N + 127) / 128) >= pairs) return run_linear_bn<128>(p, xq, ld_xq, a, out, out_dt, after, s);
   return run_linear_bn<64>(p, xq, ld_xq, a, out, out_dt, after, s);
@@ -1015,10 +1104,14 @@ avey_status launch_score_i8(const avey_linear_i8_params *p, const int8_t *xq, in
 }  // namespace
 }  // namespace avey
 
+// Up to this many rows the logits go through the workspace (32 x 768 -> 50368: 19.3 us
+// so, 21.2 with the statistics in the product; 17 x 256: 14.5 and 18.3).
+static constexpr int kLogitRows = 32;
+
 extern "C" size_t avey_score_tokens_i8_workspace_bytes(int rows, int K, int N) {
   if (rows <= 0 || K <= 0 || N <= 0) return 0;
   return quantized_bytes(rows, K) +
-         std::max(align256(static_cast<size_t>(std::min(rows, kFewRows)) * score_ld(N) * 4),
+         std::max(align256(static_cast<size_t>(std::min(rows, kLogitRows)) * score_ld(N) * 4),
                   score_partial_bytes(rows));
 }
 
@@ -1058,9 +1151,9 @@ extern "C" avey_status avey_score_tokens_i8(const avey_linear_i8_params *p, cons
       st = quantize_to_ws(p, x, x_dt, ld_x, prenorm, rows, ws, &xq, &ld_xq, &xs, s);
       if (st != AVEY_OK) return st;
     }
-    if (rows > kFewRows)
+    if (rows > (swap_pays(rows, p->N) ? kLogitRows : kFewRows))
       return launch_score_i8(p, xq, ld_xq, xs, rows, ids, logprob, stats, entropy,
-                               reinterpret_cast<float4 *>(rest), x_dt != AVEY_I8, s);
+                             reinterpret_cast<float4 *>(rest), x_dt != AVEY_I8, s);
     st = launch_linear_i8(p, xq, ld_xq, xs, rows, nullptr, 0, logits, AVEY_F32, ld, x_dt != AVEY_I8, s);
   }
   if (st != AVEY_OK) return st;

@@ -157,9 +157,11 @@ SHAPES = [(1, 768, 1000), (1, 5, 1), (2, 16, 7), (7, 31, 64), (8, 768, 257), (9,
           (30, 5000, 40), (12, 7000, 9700), (17, 64, 1), (32, 1025, 130)]
 # tiles of 128 and of 256 columns, x resident or not, several row blocks to a pair of SMs
 WIDE = [(700, 100, 4000), (2000, 300, 9001), (1500, 1100, 4004), (40000, 64, 300)]
+# few tokens against many channels
+SWAPPED = [(17, 768, 5001), (64, 1000, 9001), (33, 2100, 4743), (32, 15, 19000), (12, 1025, 4800), (9, 800, 25000)]
 
 
-@pytest.mark.parametrize("rows,K,N", SHAPES + WIDE)
+@pytest.mark.parametrize("rows,K,N", SHAPES + WIDE + SWAPPED)
 @pytest.mark.parametrize("kind,out", [("f32", "f32"), ("bf16", "bf16"), ("pair", "pair"), ("strided", "f32")])
 def test_product(rows, K, N, kind, out, cuda_dev):
     act, bias = (rows + N) % 2, K % 2 == 0
@@ -181,7 +183,7 @@ def test_product(rows, K, N, kind, out, cuda_dev):
 
 
 @pytest.mark.parametrize("rows,K,N", [(1, 64, 40), (5, 100, 13), (70, 768, 200), (300, 1536, 768),
-                                      (600, 40, 4001), (3001, 100, 2050)])
+                                      (600, 40, 4001), (3001, 100, 2050), (40, 100, 5003), (64, 65, 20000)])
 def test_residual_alone_and_in_place(rows, K, N, cuda_dev):
     lin, q, w, b = _weights(N, K, 5, cuda_dev, True)
     x = _activations(rows, K, 6)
@@ -221,9 +223,9 @@ def test_prequantized_rows_and_extreme_integers(cuda_dev):
         assert (np.abs(got - y) <= 4 * U * np.abs(y) * (1 + 1e-6)).all()
 
 
-@pytest.mark.parametrize("rows", [3, 40])
-def test_a_row_that_is_not_finite_spoils_itself_alone(rows, cuda_dev):
-    lin, q, w, b = _weights(33, 200, 9, cuda_dev, True)
+@pytest.mark.parametrize("rows,N", [(3, 33), (40, 33), (40, 4801)])
+def test_a_row_that_is_not_finite_spoils_itself_alone(rows, N, cuda_dev):
+    lin, q, w, b = _weights(N, 200, 9, cuda_dev, True)
     x = _activations(rows, 200, 10)
     clean, _ = _product(x, q, w, b, 1, None)
     x[1, 17] = np.nan

@@ -83,7 +83,7 @@ def test_one_layer_stays_near_the_16_bit_one(cuda_dev):
     assert (np.abs(D(got) - D(want)) <= bound).all()
 
 
-@pytest.mark.parametrize("rows,V,d", [(r, V, 136) for r in (1, 9, 17, 700) for V in (1, 1000, 5003)]
+@pytest.mark.parametrize("rows,V,d", [(r, V, 136) for r in (1, 9, 17, 32, 33, 700) for V in (1, 1000, 5003)]
                          + [(300, 3001, 1040), (2600, 700, 64), (40, 70000, 72)])
 def test_score_is_product_then_scores(rows, V, d, cuda_dev):
     head = _head(V, d, cuda_dev)
