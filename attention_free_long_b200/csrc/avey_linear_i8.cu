@@ -14,6 +14,8 @@
 // 256 rows of x in shared memory and walks the channels (ARES): half the bytes
 // from L2 and into shared memory, 44 instead of 48 us for 8192 x 768 x 8192 to
 // bf16.
+// Up to 64 tokens against many channels swap the operands: bound by one read of the
+// weights (32 x 768 -> 50368 to fp32: 13.0 us, 39 MB).
 #include <algorithm>
 #include <utility>
 
