@@ -158,7 +158,8 @@ SHAPES = [(1, 768, 1000), (1, 5, 1), (2, 16, 7), (7, 31, 64), (8, 768, 257), (9,
 # tiles of 128 and of 256 columns, x resident or not, several row blocks to a pair of SMs
 WIDE = [(700, 100, 4000), (2000, 300, 9001), (1500, 1100, 4004), (40000, 64, 300)]
 # few tokens against many channels
-SWAPPED = [(17, 768, 5001), (64, 1000, 9001), (33, 2100, 4743), (32, 15, 19000), (12, 1025, 4800), (9, 800, 25000)]
+SWAPPED = [(17, 768, 5001), (64, 1000, 9001), (33, 2100, 4743), (32, 15, 19000), (12, 1025, 4800), (9, 800, 25000),
+           (11, 1000, 100)]
 
 
 @pytest.mark.parametrize("rows,K,N", SHAPES + WIDE + SWAPPED)
