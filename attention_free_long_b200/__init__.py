@@ -498,20 +498,20 @@ def avey_linear_i8(x, lin: QuantLinear, act: int = AVEY_ACT_NONE,
     [rows, K], or a split pair [2, rows, K]).  residual: fp32 [rows, N].
     Returns [rows, N] of out_dtype (fp32 or bf16), or with pair=True the bf16
     split pair [2, rows, N]; rows are padded to a multiple of 8 values, so for
-    other N the result is a view.  ``out`` (fp32, bf16 or, with pair, the pair;
-    row stride a multiple of 8) is written instead when given; it may be the
-    residual.
+    other N there are gaps between them.  ``out`` (fp32, bf16 or, with pair, the
+    pair; row stride a multiple of 8) is written instead when given; it may be
+    the residual.
     """
     t, dt, rows, ld, scale = _linear_input(x, lin)
     N = lin.q.shape[0]
     if out is None:
         ld_out = (N + 7) // 8 * 8
         if pair:
-            out = t.new_empty(2, rows, ld_out, dtype=torch.bfloat16)
+            out = t.new_empty_strided((2, rows, N), (rows * ld_out, ld_out, 1), dtype=torch.bfloat16)
+        elif ld_out == N:
+            out = t.new_empty(rows, N, dtype=out_dtype)
         else:
-            out = t.new_empty(rows, ld_out, dtype=out_dtype)
-        if ld_out != N:
-            out = out[..., :N]
+            out = t.new_empty_strided((rows, N), (ld_out, 1), dtype=out_dtype)
     elif pair:
         _need(out, "out")
         if out.dtype != torch.bfloat16 or out.shape != (2, rows, N):
