@@ -134,6 +134,11 @@ avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, ave
                               const float *x_scale, int prenorm, int rows, const float *residual,
                               int64_t ld_res, void *out, avey_dtype out_dt, int64_t ld_out,
                               cudaStream_t s);
+// The same scored; ws: score_few_bytes(rows, N) bytes, 16-byte aligned.
+avey_status launch_score_few(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt, int64_t ld_x,
+                             const float *x_scale, int prenorm, int rows, const int32_t *ids, float *logprob,
+                             float *stats, float *entropy, void *ws, cudaStream_t s);
+size_t score_few_bytes(int rows, int N);
 // Arguments as avey_token_logprobs, checked by the caller (avey_logprobs.cu).
 avey_status launch_token_logprobs(const void *logits, avey_dtype dt, int rows, int V, int64_t ld,
                                   const int32_t *ids, int top, float *logprob, float *stats,

@@ -14,11 +14,14 @@
 // channels as the rows of a tile 13.5, two launches.  More rows or longer ones mean
 // more to prepare per block: from 9 rows on only up to K = 768 (12 rows against
 // 65536 x 1024: 19.4 and 17.4 us; 40000 x 2048: 27.5 and 21.7), and none from 17.
+// Scored (1 x 768 -> 50368: 12.7 us, with the logits in memory 14.9) a block leaves the
+// softmax statistics of its channels, and a block per token joins them.
 #include <algorithm>
 
 #include "avey_common.cuh"
 #include "avey_internal.h"
 #include "avey_quant.cuh"
+#include "avey_score.cuh"
 
 namespace avey {
 namespace {
@@ -36,7 +39,15 @@ struct FewArgs {
   int relu2;
   void *out;
   long long ld_out;
+  // scores: (max, sum, weighted sum) of token t over block b's words at
+  // partial[t * blocks + b], and the logits of the given tokens
+  const int32_t *ids;
+  float4 *partial;
+  float *given;
 };
+
+// What the products become besides AVEY_F32, AVEY_BF16 and AVEY_BF16X2.
+constexpr int kScore = -1;
 
 __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                        uint32_t b0, uint32_t b1) {
@@ -86,12 +97,91 @@ __device__ __forceinline__ void quantize_row_to(const FewArgs &a, int row, int8_
   }
 }
 
+// The statistics of this block's words for every token, from its warps' sums.
+template <int NB, int WARPS>
+__device__ __forceinline__ void score_block(const FewArgs &a, const int (&acc)[NB][4], const float *xs, int n0,
+                                            int warp, int lane) {
+  __shared__ float4 parts[WARPS][NB * 8];
+  const int g = lane >> 2, q = lane & 3;
+  float y[2][NB * 2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = n0 + g + 8 * h;
+    const bool in = n < a.N;
+    const float w = in ? __ldg(a.w_scale + n) : 0.f, bias = in && a.bias ? __ldg(a.bias + n) * kLog2e : 0.f;
+    const float low = in ? max_nan(bias, kMaskedWord) : kMaskedWord;
+#pragma unroll
+    for (int c = 0; c < NB * 2; ++c) {
+      const int t = (c >> 1) * 8 + 2 * q + (c & 1);
+      const float p = static_cast<float>(acc[c >> 1][2 * h + (c & 1)]) * (xs[t] * kLog2e);
+      if (in && t < a.rows && a.ids && a.ids[t] == n) a.given[t] = fmaf(p, w, bias);
+      y[h][c] = fmaf(p, w, low);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NB * 2; ++c) {
+    float m = fmaxf(fmaxf(y[0][c], y[1][c]), kLowest);
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float d0 = y[0][c] - m, d1 = y[1][c] - m, e0 = ex2(d0), e1 = ex2(d1);
+    float s = e0 + e1, t = fmaf(e0, d0, e1 * d1);
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, off);
+      t += __shfl_xor_sync(0xffffffffu, t, off);
+    }
+    if (g == 0) parts[warp][(c >> 1) * 8 + 2 * q + (c & 1)] = make_float4(m, s, t, 0.f);
+  }
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t < a.rows) {
+    Stat2 st{kLowest, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) join2(st, Stat2{parts[i][t].x, parts[i][t].y, parts[i][t].z});
+    a.partial[static_cast<long long>(t) * gridDim.x + blockIdx.x] = make_float4(st.m, st.s, st.t, 0.f);
+  }
+  grid_release();
+}
+
+constexpr int kJoinThreads = 256;
+
+// One block per token: joins its blocks' statistics.
+__global__ void __launch_bounds__(kJoinThreads)
+    score_few_join(int N, int blocks, const int32_t *ids, const float4 *partial,
+                   const float *given, float *logprob, float *stats, float *entropy, int *status) {
+  __shared__ float4 parts[kJoinThreads / 32];
+  const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_wait();
+  Stat2 st{kLowest, 0.f, 0.f};
+  for (int i = threadIdx.x; i < blocks; i += kJoinThreads) {
+    const float4 v = partial[static_cast<long long>(row) * blocks + i];
+    join2(st, Stat2{v.x, v.y, v.z});
+  }
+  rebase2(st, warp_max(st.m));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
+    st.t += __shfl_xor_sync(0xffffffffu, st.t, off);
+  }
+  if (lane == 0) parts[warp] = make_float4(st.m, st.s, st.t, 0.f);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int i = 1; i < kJoinThreads / 32; ++i) join2(st, Stat2{parts[i].x, parts[i].y, parts[i].z});
+  int id = ids ? ids[row] : -1;
+  if (id >= N) {
+    record_status(status, AVEY_ERR_DEVICE_BOUNDS);
+    id = -1;
+  }
+  write_scores(st, row, id >= 0, id >= 0 ? given[row] : 0.f, logprob, stats, entropy);
+}
+
 // NB blocks of eight tokens, WARPS x 16 channels a block, DT the type of x.
-// Two blocks of tokens: four thread blocks an SM, or from 56832 channels on some
-// wait and prepare the tokens after the others (12 x 768 -> 65536: 19.9 us with three
-// an SM, 15.7 with four; 50368: 12.9 and 13.4).
+// Four thread blocks an SM, or from 56832 channels on some wait and prepare the
+// tokens after the others (12 x 768 -> 65536: 19.9 us with three an SM, 15.7 with
+// four; 50368: 12.9 and 13.4; 1 x 1024 -> 65536: 20.2 and 15.8).
 template <int NB, int WARPS, int DT, int OUT>
-__global__ void __launch_bounds__(WARPS * 32, NB == 2 && WARPS == 8 ? 4 : 0) linear_i8_few(const FewArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 4 : 0) linear_i8_few(const FewArgs a) {
   extern __shared__ __align__(16) int8_t xs_q[];
   __shared__ float xs[NB * 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -135,7 +225,7 @@ __global__ void __launch_bounds__(WARPS * 32, NB == 2 && WARPS == 8 ? 4 : 0) lin
     }
   }
   __syncthreads();
-  if (n0 >= a.N) return;
+  if (OUT != kScore && n0 >= a.N) return;
 
   int acc[NB][4] = {};
   const int8_t *w0 = a.Wq + static_cast<long long>(min(n0 + g, a.N - 1)) * a.ld_w + q * 16;
@@ -163,6 +253,10 @@ __global__ void __launch_bounds__(WARPS * 32, NB == 2 && WARPS == 8 ? 4 : 0) lin
         mma_s8(acc[b], u[i].z, v[i].z, u[i].w, v[i].w, x.z, x.w);
       }
     }
+  }
+  if constexpr (OUT == kScore) {
+    score_block<NB, WARPS>(a, acc, xs, n0, warp, lane);
+    return;
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -198,6 +292,14 @@ __global__ void __launch_bounds__(WARPS * 32, NB == 2 && WARPS == 8 ? 4 : 0) lin
   }
 }
 
+// Four warps a block while that leaves SMs without one; eight share the
+// preparation of the tokens among more channels.
+inline int few_warps(int N) { return N <= 64 * sm_count() ? 4 : 8; }
+inline int few_grid(int N) {
+  const int channels = 16 * few_warps(N);
+  return (N + channels - 1) / channels;
+}
+
 template <int NB, int WARPS, int DT, int OUT>
 avey_status run_few(const FewArgs &a, cudaStream_t s) {
   auto kern = linear_i8_few<NB, WARPS, DT, OUT>;
@@ -210,21 +312,20 @@ avey_status run_few(const FewArgs &a, cudaStream_t s) {
       return AVEY_ERR_CUDA;
     }
   }
-  kern<<<(a.N + 16 * WARPS - 1) / (16 * WARPS), WARPS * 32, bytes, s>>>(a);
+  kern<<<few_grid(a.N), WARPS * 32, bytes, s>>>(a);
   AVEY_CHECK_LAUNCH("linear_i8_few", s);
   return AVEY_OK;
 }
 
 template <int NB, int DT, int OUT>
 avey_status run_few_warps(const FewArgs &a, cudaStream_t s) {
-  // four warps a block while that leaves SMs without one; eight share the
-  // preparation of the tokens among more channels
-  if (a.N <= 64 * sm_count()) return run_few<NB, 4, DT, OUT>(a, s);
+  if (few_warps(a.N) == 4) return run_few<NB, 4, DT, OUT>(a, s);
   return run_few<NB, 8, DT, OUT>(a, s);
 }
 
 template <int NB, int DT>
-avey_status run_few_out(const FewArgs &a, avey_dtype out_dt, cudaStream_t s) {
+avey_status run_few_out(const FewArgs &a, int out_dt, cudaStream_t s) {
+  if (out_dt == kScore) return run_few_warps<NB, DT, kScore>(a, s);
   if (out_dt == AVEY_F32) return run_few_warps<NB, DT, AVEY_F32>(a, s);
   if (out_dt == AVEY_BF16) return run_few_warps<NB, DT, AVEY_BF16>(a, s);
   return run_few_warps<NB, DT, AVEY_BF16X2>(a, s);
@@ -245,10 +346,10 @@ bool linear_few_quantizes(avey_dtype x_dt, int rows, int K) {
   return x_dt != AVEY_I8 && linear_few_fits(rows, K);
 }
 
-avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt, int64_t ld_x,
-                              const float *x_scale, int prenorm, int rows, const float *residual,
-                              int64_t ld_res, void *out, avey_dtype out_dt, int64_t ld_out,
-                              cudaStream_t s) {
+namespace {
+
+FewArgs few_args(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt, int64_t ld_x,
+                 const float *x_scale, int prenorm, int rows) {
   FewArgs a{};
   a.x = x;
   a.ld_x = ld_x;
@@ -263,12 +364,12 @@ avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, ave
   a.ld_w = p->ld_w;
   a.w_scale = p->w_scale;
   a.bias = p->bias;
-  a.residual = residual;
-  a.ld_res = ld_res;
   a.relu2 = p->act == AVEY_ACT_RELU2;
-  a.out = out;
-  a.ld_out = ld_out;
-  const bool one = few_blocks(rows) == 1;
+  return a;
+}
+
+avey_status run_few_any(const FewArgs &a, avey_dtype x_dt, int out_dt, cudaStream_t s) {
+  const bool one = few_blocks(a.rows) == 1;
 #define AVEY_FEW(DT) return one ? run_few_out<1, DT>(a, out_dt, s) : run_few_out<2, DT>(a, out_dt, s)
   switch (x_dt) {
     case AVEY_F32: AVEY_FEW(AVEY_F32);
@@ -277,6 +378,45 @@ avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, ave
     default: AVEY_FEW(AVEY_I8);
   }
 #undef AVEY_FEW
+}
+
+}  // namespace
+
+avey_status launch_linear_few(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt, int64_t ld_x,
+                              const float *x_scale, int prenorm, int rows, const float *residual,
+                              int64_t ld_res, void *out, avey_dtype out_dt, int64_t ld_out,
+                              cudaStream_t s) {
+  FewArgs a = few_args(p, x, x_dt, ld_x, x_scale, prenorm, rows);
+  a.residual = residual;
+  a.ld_res = ld_res;
+  a.out = out;
+  a.ld_out = ld_out;
+  return run_few_any(a, x_dt, out_dt, s);
+}
+
+size_t score_few_bytes(int rows, int N) {
+  return static_cast<size_t>(rows) * few_grid(N) * sizeof(float4) + static_cast<size_t>(rows) * sizeof(float);
+}
+
+avey_status launch_score_few(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt, int64_t ld_x,
+                             const float *x_scale, int prenorm, int rows, const int32_t *ids, float *logprob,
+                             float *stats, float *entropy, void *ws, cudaStream_t s) {
+  FewArgs a = few_args(p, x, x_dt, ld_x, x_scale, prenorm, rows);
+  const int blocks = few_grid(p->N);
+  a.ids = ids;
+  a.partial = static_cast<float4 *>(ws);
+  a.given = reinterpret_cast<float *>(a.partial + static_cast<size_t>(rows) * blocks);
+  const avey_status st = run_few_any(a, x_dt, kScore, s);
+  if (st != AVEY_OK) return st;
+  const cudaError_t e = launch_after(score_few_join, static_cast<unsigned>(rows), kJoinThreads, 0, s, p->N, blocks,
+                                     ids, a.partial, a.given, logprob, stats, entropy, device_status_word());
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    set_detail("score_few_join launch failed: %s", cudaGetErrorString(e));
+    return AVEY_ERR_CUDA;
+  }
+  AVEY_CHECK_LAUNCH("score_few_join", s);
+  return AVEY_OK;
 }
 
 }  // namespace avey

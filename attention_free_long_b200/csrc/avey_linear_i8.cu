@@ -21,6 +21,7 @@
 
 #include "avey_common.cuh"
 #include "avey_internal.h"
+#include "avey_score.cuh"
 
 namespace avey {
 namespace {
@@ -28,10 +29,6 @@ namespace {
 constexpr int kBK = 128;
 // K steps of x that fit beside a ring of three stages at least
 constexpr int kResidentSteps = 8;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLowest = -3.402823466e38f;
-constexpr float kFar2 = -200.0f;  // ex2 is 0 in fp32 from here down
-constexpr float kMaskedWord = -1e30f;
 
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -154,22 +151,6 @@ __device__ __forceinline__ void ld_shared4(uint32_t addr, float (&r)[4]) {
                : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
                : "r"(addr)
                : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// (max, sum 2^(y - max), sum 2^(y - max) (y - max)) of values y in units of log 2
-struct Stat2 {
-  float m, s, t;
-};
-__device__ __forceinline__ void rebase2(Stat2 &a, float M) {
-  const float d = a.m - M, f = ex2(d);
-  a.t = f * fmaf(a.s, fmaxf(d, kFar2), a.t);
-  a.s *= f;
-  a.m = M;
 }
 
 // First tile of pair p's share: shares are contiguous in the order (row block,
@@ -1015,12 +996,7 @@ __global__ void __launch_bounds__(256)
   const int parts = G * static_cast<int>(p1 - p0 + 1);
   for (int i = lane; i < parts; i += 32) {
     const float4 v = a.partial[((p0 + i / G + mt) * G + i % G) * 256 + (row & 255)];
-    Stat2 o{v.x, v.y, v.z};
-    const float M = fmaxf(st.m, o.m);
-    rebase2(st, M);
-    rebase2(o, M);
-    st.s += o.s;
-    st.t += o.t;
+    join2(st, Stat2{v.x, v.y, v.z});
   }
   rebase2(st, warp_max(st.m));
   int id = ids ? ids[row] : -1;
@@ -1044,23 +1020,11 @@ __global__ void __launch_bounds__(256)
     acc += __shfl_xor_sync(0xffffffffu, acc, off);
   }
   if (lane != 0) return;
-  const bool empty = st.m <= 0.5f * kMaskedWord;
-  const bool bad = !(st.s < INFINITY) || st.m == INFINITY;
-  const float nan = __uint_as_float(0x7fc00000u);
-  const float z = logf(st.s);
-  if (logprob) {
-    float lp = 0.f;
-    if (id >= 0) {
-      const float y = fmaf(static_cast<float>(acc) * (a.x_scale[row] * kLog2e), a.w_scale[id],
-                           a.bias ? a.bias[id] * kLog2e : 0.f);
-      lp = bad ? nan : empty ? -INFINITY : fmaf(y - st.m, kLn2, -z);
-    }
-    logprob[row] = lp;
-  }
-  if (stats)
-    reinterpret_cast<float2 *>(stats)[row] =
-        bad ? make_float2(nan, nan) : empty ? make_float2(-INFINITY, 0.f) : make_float2(st.m * kLn2, z);
-  if (entropy) entropy[row] = bad ? nan : empty ? 0.f : fmaf(-kLn2, st.t / st.s, z);
+  float y = 0.f;
+  if (id >= 0)
+    y = fmaf(static_cast<float>(acc) * (a.x_scale[row] * kLog2e), a.w_scale[id],
+             a.bias ? a.bias[id] * kLog2e : 0.f);
+  write_scores(st, row, id >= 0, y, logprob, stats, entropy);
 }
 
 inline int64_t score_ld(int N) { return (static_cast<int64_t>(N) + 7) / 8 * 8; }
@@ -1114,7 +1078,7 @@ extern "C" size_t avey_score_tokens_i8_workspace_bytes(int rows, int K, int N) {
   if (rows <= 0 || K <= 0 || N <= 0) return 0;
   return quantized_bytes(rows, K) +
          std::max(align256(static_cast<size_t>(std::min(rows, kLogitRows)) * score_ld(N) * 4),
-                  score_partial_bytes(rows));
+                  std::max(score_partial_bytes(rows), score_few_bytes(std::min(rows, kFewRows), N)));
 }
 
 extern "C" avey_status avey_score_tokens_i8(const avey_linear_i8_params *p, const void *x, avey_dtype x_dt,
@@ -1141,23 +1105,21 @@ extern "C" avey_status avey_score_tokens_i8(const avey_linear_i8_params *p, cons
                need);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char *rest = static_cast<char *>(ws) + quantized_bytes(rows, p->K);
+  if (linear_few_fits(rows, p->K))
+    return launch_score_few(p, x, x_dt, ld_x, x_scale, prenorm ? 1 : 0, rows, ids, logprob, stats, entropy, rest, s);
   float *logits = reinterpret_cast<float *>(rest);
   const int64_t ld = score_ld(p->N);
-  if (linear_few_quantizes(x_dt, rows, p->K)) {
-    st = launch_linear_few(p, x, x_dt, ld_x, nullptr, prenorm ? 1 : 0, rows, nullptr, 0, logits, AVEY_F32, ld, s);
-  } else {
-    const int8_t *xq = static_cast<const int8_t *>(x);
-    const float *xs = x_scale;
-    int64_t ld_xq = ld_x;
-    if (x_dt != AVEY_I8) {
-      st = quantize_to_ws(p, x, x_dt, ld_x, prenorm, rows, ws, &xq, &ld_xq, &xs, s);
-      if (st != AVEY_OK) return st;
-    }
-    if (rows > (swap_pays(rows, p->N) ? kLogitRows : kFewRows))
-      return launch_score_i8(p, xq, ld_xq, xs, rows, ids, logprob, stats, entropy,
-                             reinterpret_cast<float4 *>(rest), x_dt != AVEY_I8, s);
-    st = launch_linear_i8(p, xq, ld_xq, xs, rows, nullptr, 0, logits, AVEY_F32, ld, x_dt != AVEY_I8, s);
+  const int8_t *xq = static_cast<const int8_t *>(x);
+  const float *xs = x_scale;
+  int64_t ld_xq = ld_x;
+  if (x_dt != AVEY_I8) {
+    st = quantize_to_ws(p, x, x_dt, ld_x, prenorm, rows, ws, &xq, &ld_xq, &xs, s);
+    if (st != AVEY_OK) return st;
   }
+  if (rows > (swap_pays(rows, p->N) ? kLogitRows : kFewRows))
+    return launch_score_i8(p, xq, ld_xq, xs, rows, ids, logprob, stats, entropy,
+                           reinterpret_cast<float4 *>(rest), x_dt != AVEY_I8, s);
+  st = launch_linear_i8(p, xq, ld_xq, xs, rows, nullptr, 0, logits, AVEY_F32, ld, x_dt != AVEY_I8, s);
   if (st != AVEY_OK) return st;
   return launch_token_logprobs(logits, AVEY_F32, rows, p->N, ld, ids, 0, logprob, stats, entropy, nullptr,
                                nullptr, s);

@@ -84,7 +84,8 @@ def test_one_layer_stays_near_the_16_bit_one(cuda_dev):
 
 
 @pytest.mark.parametrize("rows,V,d", [(r, V, 136) for r in (1, 9, 17, 32, 33, 700) for V in (1, 1000, 5003)]
-                         + [(300, 3001, 1040), (2600, 700, 64), (40, 70000, 72)])
+                         + [(300, 3001, 1040), (2600, 700, 64), (40, 70000, 72), (1, 50368, 768), (8, 20011, 1025),
+                            (16, 60001, 100), (12, 9000, 1100)])
 def test_score_is_product_then_scores(rows, V, d, cuda_dev):
     head = _head(V, d, cuda_dev)
     g = torch.Generator(device=cuda_dev).manual_seed(rows)
@@ -130,7 +131,7 @@ def test_score_many_rows_in_a_small_workspace(cuda_dev):
 
 def test_score_spoilt_and_ignored_rows(cuda_dev):
     head = _head(2000, 64, cuda_dev)
-    for rows in (4, 300):
+    for rows in (4, 20, 300):
         h = torch.randn(rows, 64, device=cuda_dev)
         ids = torch.full((rows,), 5, dtype=torch.int32, device=cuda_dev)
         ids[1], ids[2] = -1, 2000
