@@ -235,14 +235,18 @@ __device__ __forceinline__ void lin_values_swapped(float (&v)[32], float ws, flo
 
 // A 32 x 32 chunk of channels x tokens: each token's 32 channels are one store.
 template <int OUT>
-__device__ __forceinline__ void store_swapped(const LinArgs &a, int channel, int token0, const float (&v)[32]) {
+__device__ __forceinline__ void store_swapped(const LinArgs &a, int channel, int token0, float (&v)[32]) {
+  if (OUT == AVEY_F32 && a.residual) {  // all loads before the first store, which it might be
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (token0 + j < a.N) v[j] += a.residual[static_cast<long long>(token0 + j) * a.ld_res + channel];
+  }
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     const long long t = token0 + j;
     if (t >= a.N) break;
-    float y = v[j];
+    const float y = v[j];
     if constexpr (OUT == AVEY_F32) {
-      if (a.residual) y += a.residual[t * a.ld_res + channel];
       static_cast<float *>(a.out)[t * a.ld_out + channel] = y;
     } else {
       bf16 *hi = static_cast<bf16 *>(a.out) + t * a.ld_out + channel;
@@ -552,7 +556,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
     // The residual of a chunk into staging buffer `to`, a chunk ahead.
     uint32_t coming = 0;  // buffers with a copy in flight
     auto fetch_residual = [&](int row0, int col0, int to) {
-      if (col0 >= a.N_tma || !a.res_tma) return;
+      if (!a.res_tma) {
+        // a row's 32 columns at a time, four bytes a lane
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+        const int n = min(32, a.rows - row0);
+        const float *r = a.residual + row0 * a.ld_res + col0 + lane;
+        const uint32_t at = stg + to * P::BUF + (lane & 3) * 4;
+        if (col0 + lane < a.N) {
+#pragma unroll 8
+          for (int j = 0; j < n; ++j) cp_async4(at + lin_sw128(j, lane >> 2), r + j * a.ld_res);
+        }
+        cp_async_commit();
+        return;
+      }
+      if (col0 >= a.N_tma) return;
       if (lane == 0) {
         bulk_wait_read<1>();  // the store from this buffer, three chunks ago at least, has read it
         mbar_arrive_expect_tx(res_bar(ew, to), P::BUF);
@@ -624,15 +642,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
         } else {
           lin_values(v, xs, w_s, b_s, a.relu2);
           __syncwarp();
-          if (RES && !a.res_tma && valid) {
-            const float *r = a.residual + row * a.ld_res;
+          const uint32_t at = stg + this_buf * P::BUF;
+          auto add_residual = [&]() {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col0 + j < a.N) v[j] += r[col0 + j];
+            for (int c = 0; c < 8; ++c) {
+              float r[4];
+              ld_shared4(at + lin_sw128(lane, c), r);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[4 * c + j] += r[j];
+            }
+          };
+          if (RES && !a.res_tma) {
+            // all but the copies of the next chunk, which are under way if it has been fetched
+            if (have)
+              cp_async_wait<1>();
+            else
+              cp_async_wait<0>();
+            __syncwarp();
+            add_residual();
           }
           if (col0 + 32 > a.N_tma && valid) store_rest<OUT, RES>(a, row, col0, v);
           if (col0 < a.N_tma) {  // warp-uniform
-            const uint32_t at = stg + this_buf * P::BUF;
             if (RES && a.res_tma) {
               if (!warp_wait(res_bar(ew, this_buf), res_phase >> this_buf & 1u, abort_flag)) {
                 ok = false;
@@ -640,13 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
               }
               res_phase ^= 1u << this_buf;
               coming &= ~(1u << this_buf);
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                float r[4];
-                ld_shared4(at + lin_sw128(lane, c), r);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[4 * c + j] += r[j];
-              }
+              add_residual();
             } else {
               // the last store issued from this buffer must have read it
               if (lane == 0) bulk_wait_read<P::BUFS - 1>();
@@ -705,6 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
       record_status(a.status, AVEY_ERR_DEVICE_TIMEOUT);
       if constexpr (RES) {
         // residual copies in flight must land before the block leaves
+        cp_async_wait<0>();
         if (lane == 0)
           for (int i = 0; i < P::BUFS; ++i)
             if (coming >> i & 1u) drain_wait(res_bar(ew, i), res_phase >> i & 1u);
