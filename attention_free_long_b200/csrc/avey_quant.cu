@@ -100,8 +100,10 @@ avey_status run_quantize(const void *x, int rows, int cols, long long ld_x, int8
     AVEY_QUANTIZE(128);
   else if (cols > 32 * 32)
     AVEY_QUANTIZE(64);
-  else if (cols > 8 * 32)
+  else if (cols > 16 * 32)
     AVEY_QUANTIZE(32);
+  else if (cols > 8 * 32)
+    AVEY_QUANTIZE(16);
   else
     AVEY_QUANTIZE(8);
 #undef AVEY_QUANTIZE
