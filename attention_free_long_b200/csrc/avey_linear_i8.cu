@@ -260,38 +260,46 @@ __device__ __forceinline__ void store_swapped(const LinArgs &a, int channel, int
   }
 }
 
-// A 32-column chunk into a row's running statistics.
-__device__ __forceinline__ void score_values(float (&v)[32], float xs, const float *w, const float *b,
-                                             Stat2 &st) {
+// A pair of sums of columns 2 j, 2 j + 1 as logits in units of log 2.
+__device__ __forceinline__ float2 score_pair(uint32_t r0, uint32_t r1, float xs, const float *w, const float *b, int j) {
+  const float2 f = make_float2(static_cast<float>(static_cast<int>(r0)), static_cast<float>(static_cast<int>(r1)));
+  return ffma2(fmul2(f, make_float2(xs, xs)), *reinterpret_cast<const float2 *>(w + 2 * j),
+               *reinterpret_cast<const float2 *>(b + 2 * j));
+}
+
+// A tile's columns of this warp into a row's running statistics, 16 at a time: the
+// exponentials of one part are computed among the logits of the next, so that
+// neither the exponential unit nor the others wait for a whole part.
+template <int PARTS>
+__device__ __forceinline__ void score_tile(uint32_t taddr, uint32_t step, float xs, const float *cols, Stat2 &st) {
+  uint32_t raw[16];
+  float2 y[8];
+  tmem_ld16(taddr, raw);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const float4 w4 = *reinterpret_cast<const float4 *>(w + 4 * q);
-    const float4 b4 = *reinterpret_cast<const float4 *>(b + 4 * q);
-    const float2 x2 = make_float2(xs, xs);
+  for (int j = 0; j < 8; ++j) y[j] = score_pair(raw[2 * j], raw[2 * j + 1], xs, cols, cols + 32, j);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float2 f = make_float2(static_cast<float>(__float_as_int(v[4 * q + 2 * h])),
-                                   static_cast<float>(__float_as_int(v[4 * q + 2 * h + 1])));
-      const float2 y = ffma2(fmul2(f, x2), h ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y),
-                             h ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y));
-      v[4 * q + 2 * h] = y.x;
-      v[4 * q + 2 * h + 1] = y.y;
+  for (int h = 0; h < PARTS; ++h) {
+    float m = st.m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max3f(m, y[j].x, y[j].y);
+    rebase2(st, m);
+    const float2 minus = make_float2(-m, -m);
+    float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, t[2] = {s[0], s[0]};
+    if (h + 1 < PARTS) tmem_ld16(taddr + ((h + 1) >> 1) * step + ((h + 1) & 1) * 16, raw);
+    const float *w = cols + ((h + 1) >> 1) * 64 + ((h + 1) & 1) * 16;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 d = fadd2(y[j], minus);
+      const float2 e = make_float2(ex2(d.x), ex2(d.y));
+      if (h + 1 < PARTS) y[j] = score_pair(raw[2 * j], raw[2 * j + 1], xs, w, w + 32, j);
+      s[j & 1] = fadd2(s[j & 1], e);
+      t[j & 1] = ffma2(e, d, t[j & 1]);
     }
+    s[0] = fadd2(s[0], s[1]);
+    t[0] = fadd2(t[0], t[1]);
+    st.s += s[0].x + s[0].y;
+    st.t += t[0].x + t[0].y;
   }
-  rebase2(st, fmaxf(st.m, max32(v)));
-  const float2 minus = make_float2(-st.m, -st.m);
-  float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, t[2] = {s[0], s[0]};
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float2 d = fadd2(make_float2(v[2 * j], v[2 * j + 1]), minus);
-    const float2 e = make_float2(ex2(d.x), ex2(d.y));
-    s[j & 1] = fadd2(s[j & 1], e);
-    t[j & 1] = ffma2(e, d, t[j & 1]);
-  }
-  s[0] = fadd2(s[0], s[1]);
-  t[0] = fadd2(t[0], t[1]);
-  st.s += s[0].x + s[0].y;
-  st.t += t[0].x + t[0].y;
 }
 
 // SWAP: few tokens against many channels.  The channels are the rows (A), the
@@ -608,11 +616,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
       tc_fence_after();
       const uint32_t taddr =
           tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
+      if constexpr (OUT == kScore) {
+        // words past the last have their value
+        if (row0 < a.rows) score_tile<2 * P::CHUNKS>(taddr + group * 32, P::GROUPS * 32, xs, cols, st);
+      }
 #pragma unroll 1
-      for (int ch = group, i = 0; ch < BN / 32; ch += P::GROUPS, ++i) {
+      for (int ch = OUT == kScore ? BN / 32 : group; ch < BN / 32; ch += P::GROUPS) {
         const int col0 = nt * BN + ch * 32;
         if (col0 >= a.N || row0 >= a.rows) break;  // warp-uniform
-        const float *w_s = cols + (OUT == kScore ? i * 64 : 0), *b_s = w_s + 32;
+        const float *w_s = cols, *b_s = w_s + 32;
         const int this_buf = buf;
         if constexpr (P::BUFS > 1) buf = buf + 1 == P::BUFS ? 0 : buf + 1;
         if constexpr (OUT != kScore) {
@@ -633,9 +645,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LinLayout<BN, OUT, R
         }
         float v[32];
         tmem_ld32(taddr + ch * 32, v);
-        if constexpr (OUT == kScore) {
-          score_values(v, xs, w_s, b_s, st);
-        } else if constexpr (SWAP) {
+        if constexpr (SWAP) {
           lin_values_swapped(v, xs, bs, w_s, a.relu2);
           __syncwarp();
           if (valid) store_swapped<OUT>(a, row, col0, v);
