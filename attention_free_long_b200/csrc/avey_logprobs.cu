@@ -580,6 +580,12 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? (B == 4 ? 10 :
   uint32_t sorted = 0;
   if constexpr (TOP) {
     sorted = warp_largest(ord_of(best.first), a.top, lane);
+    if (a.top > 8 && r.vecs > B * stride) {
+      // other elements than the first ones, so that many alternatives too have a bar
+      // that few elements reach (14781 x 9171 bf16, 32 of them: 219 -> 136 us)
+      const uint32_t second = warp_sort(ord_of(best.second), 32, lane);
+      sorted = merge_reversed<32>(sorted, __shfl_xor_sync(0xffffffffu, second, 31), lane);
+    }
     if (W > 1) maxima[warp][lane] = sorted;
   }
   Stat all = row_stats<W>(st, sm, warp, lane);
