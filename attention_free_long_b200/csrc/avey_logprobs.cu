@@ -527,7 +527,8 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t a) {
 // CLUSTER, a cluster of a.blocks blocks, block `rank` taking the vectors u with
 // u / (32 W) % blocks == rank.
 template <typename T, bool TOP, int W, int B, bool CLUSTER>
-__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? (B == 4 ? 10 : 8) : 32 / W) token_logprobs(const LpArgs a) {
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? (B == 4 ? 10 : 8) : 32 / W)
+    token_logprobs(const LpArgs a) {
   constexpr int N = Vec<T>::N;
   static_assert(!CLUSTER || W == 8, "clusters are made of blocks of eight warps");
   __shared__ float sm[3][W];
@@ -636,7 +637,8 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? (B == 4 ? 10 :
   const RowResult res(all);
   if (writer) write_row(a, row, res, id, x_id);
   if constexpr (TOP) {
-    uint64_t key = select_top<T, B>(r, rank * 32 * W + warp * 32, stride, best, bar, a.top, queues[W == 1 ? threadIdx.x >> 5 : warp], lane);
+    uint64_t key = select_top<T, B>(r, rank * 32 * W + warp * 32, stride, best, bar, a.top,
+                                    queues[W == 1 ? threadIdx.x >> 5 : warp], lane);
     if constexpr (W > 1) {
       lists[warp][lane] = key;
       __syncthreads();
