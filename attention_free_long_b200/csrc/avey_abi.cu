@@ -129,10 +129,17 @@ static bool encode_typed(CUtensorMap *map, CUtensorMapDataType type, const void 
   const CUtensorMapSwizzle sw = swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                 : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                       : CU_TENSOR_MAP_SWIZZLE_NONE;
-  CUresult r = fn(map, type, 3,
-                  const_cast<void *>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const auto encode = [&] {
+    return fn(map, type, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    // The thread's first CUDA call: the runtime makes its device's context
+    // current only with a call that needs one, the driver does not.
+    const int dev = current_device();
+    if (dev >= 0 && cudaSetDevice(dev) == cudaSuccess) r = encode();
+  }
   if (r != CUDA_SUCCESS) {
     set_detail("cuTensorMapEncodeTiled failed (%d): inner=%llu rows=%llu batch=%llu box=%ux%u", int(r),
                (unsigned long long)inner, (unsigned long long)rows, (unsigned long long)batch,
