@@ -304,7 +304,9 @@ template <int NB, int WARPS, int DT, int OUT>
 avey_status run_few(const FewArgs &a, cudaStream_t s) {
   auto kern = linear_i8_few<NB, WARPS, DT, OUT>;
   const int bytes = NB * 8 * a.stride;
-  if (bytes > 48 * 1024) {
+  // static arrays (the scales, the scores' parts) count toward the 48 KB that need no request
+  constexpr int kStatic = NB * 8 * 4 + (OUT == kScore ? WARPS * NB * 8 * static_cast<int>(sizeof(float4)) : 0);
+  if (bytes + kStatic > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) {
       cudaGetLastError();
