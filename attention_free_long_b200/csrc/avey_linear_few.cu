@@ -300,6 +300,8 @@ inline int few_grid(int N) {
   return (N + channels - 1) / channels;
 }
 
+constexpr int kFewShared = 96 * 1024;  // at most two blocks' worth of an SM
+
 template <int NB, int WARPS, int DT, int OUT>
 avey_status run_few(const FewArgs &a, cudaStream_t s) {
   auto kern = linear_i8_few<NB, WARPS, DT, OUT>;
@@ -307,7 +309,9 @@ avey_status run_few(const FewArgs &a, cudaStream_t s) {
   // static arrays (the scales, the scores' parts) count toward the 48 KB that need no request
   constexpr int kStatic = NB * 8 * 4 + (OUT == kScore ? WARPS * NB * 8 * static_cast<int>(sizeof(float4)) : 0);
   if (bytes + kStatic > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // the limit is the kernel's, whichever thread calls it: always the largest, so that no
+    // call lowers another's before its launch
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewShared);
     if (e != cudaSuccess) {
       cudaGetLastError();
       set_detail("linear_i8_few: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -332,8 +336,6 @@ avey_status run_few_out(const FewArgs &a, int out_dt, cudaStream_t s) {
   if (out_dt == AVEY_BF16) return run_few_warps<NB, DT, AVEY_BF16>(a, s);
   return run_few_warps<NB, DT, AVEY_BF16X2>(a, s);
 }
-
-constexpr int kFewShared = 96 * 1024;  // at most two blocks' worth of an SM
 
 inline int few_stride(int K) { return (K + 127) / 128 * 128 + 64; }  // odd multiples of 64: no bank conflicts
 inline int few_blocks(int rows) { return rows <= 8 ? 1 : 2; }

@@ -86,6 +86,12 @@ struct LinLayout {
   static constexpr uint32_t tiles_bytes(int ksteps) {
     return (ARES ? ksteps * A_BYTES : 0) + stages(ksteps) * STAGE_BYTES;
   }
+  // the most that any number of K steps takes
+  static constexpr uint32_t max_bytes() {
+    uint32_t most = 0;
+    for (int k = 1; k <= kResidentSteps; ++k) most = tiles_bytes(k) > most ? tiles_bytes(k) : most;
+    return most + REST_BYTES;
+  }
   static_assert(stages(ARES ? kResidentSteps : 1) >= 3, "shared memory budget");
 };
 
@@ -771,7 +777,10 @@ avey_status run_linear_pair(const CUtensorMap &ma, const CUtensorMap &mb, const 
   a.stages = P::stages(ksteps);
   a.tiles_bytes = P::tiles_bytes(ksteps);
   const uint32_t bytes = a.tiles_bytes + P::REST_BYTES;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  // the limit is the kernel's, whichever thread calls it: always the largest, so that no
+  // call lowers another's before its launch
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(P::max_bytes()));
   if (e != cudaSuccess) {
     cudaGetLastError();
     set_detail("linear_i8: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
