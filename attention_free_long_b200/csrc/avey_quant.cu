@@ -166,7 +166,8 @@ extern "C" avey_status avey_quantize_rows(const void *x, avey_dtype dt, int rows
     const uintptr_t n = static_cast<uintptr_t>(rows - 1), es = dt == AVEY_F32 ? 4 : 2;
     const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), q0 = reinterpret_cast<uintptr_t>(q);
     const uintptr_t xn = x0 + (n * ld_x + cols + (dt == AVEY_BF16X2 ? rows * ld_x : 0)) * es;
-    AVEY_REQUIRE(xn <= q0 || q0 + n * ld_q + cols <= x0, AVEY_ERR_INVALID_ARG, "avey_quantize_rows: q overlaps x");
+    const uintptr_t qn = q0 + n * ld_q + (cols + 15) / 16 * 16;  // with the zeros behind its last row
+    AVEY_REQUIRE(xn <= q0 || qn <= x0, AVEY_ERR_INVALID_ARG, "avey_quantize_rows: q overlaps x");
   }
   return launch_quantize_rows(x, dt, rows, cols, ld_x, prenorm ? 1 : 0, q, ld_q, scale,
                               reinterpret_cast<cudaStream_t>(stream));
