@@ -111,6 +111,22 @@ avey_status launch_long_mix_tc(const bf16 *a_hi, const bf16 *a_lo, bool a_batche
                                bf16 *clo, cudaStream_t s);
 
 // ---- 8-bit products and token scoring ----
+// Rows of `width` bytes every `stride` bytes (stride >= width, rows >= 1).
+struct ByteRows {
+  uintptr_t at;
+  uint64_t rows, width, stride;
+  uintptr_t end() const { return at + (rows - 1) * stride + width; }
+};
+// Whether the two share a byte.  Rows that alternate, as the columns of one
+// buffer do, share none; alternating rows of unlike strides count as sharing.
+inline bool rows_overlap(ByteRows a, ByteRows b) {
+  if (a.end() <= b.at || b.end() <= a.at) return false;
+  if (a.rows == 1) a.stride = b.stride;
+  if (b.rows == 1) b.stride = a.stride;
+  if (a.stride != b.stride) return true;
+  const uint64_t s = a.stride, d = b.at >= a.at ? (b.at - a.at) % s : (s - (a.at - b.at) % s) % s;
+  return d < a.width || d + b.width > s;  // b's rows begin d bytes after one of a's
+}
 // Checks of a source to be quantised (avey_quant.cu); fn names the entry point.
 avey_status check_quant_source(const char *fn, const void *x, avey_dtype dt, int cols, int64_t ld_x);
 avey_status launch_quantize_rows(const void *x, avey_dtype dt, int rows, int cols, int64_t ld_x,

@@ -982,16 +982,14 @@ extern "C" avey_status avey_linear_i8(const avey_linear_i8_params *p, const void
   AVEY_REQUIRE(aligned16(out) && (reinterpret_cast<uintptr_t>(residual) & 3) == 0, AVEY_ERR_INVALID_ARG,
                "%s: out must be 16-byte and the residual 4-byte aligned", fn);
   {
-    const uintptr_t n = static_cast<uintptr_t>(rows - 1), o = reinterpret_cast<uintptr_t>(out);
-    const uintptr_t oes = out_dt == AVEY_F32 ? 4 : 2, xes = x_dt == AVEY_I8 ? 1 : x_dt == AVEY_F32 ? 4 : 2;
-    const uintptr_t on = (n * ld_out + p->N + (out_dt == AVEY_BF16X2 ? rows * ld_out : 0)) * oes;
-    const uintptr_t xn = (n * ld_x + p->K + (x_dt == AVEY_BF16X2 ? rows * ld_x : 0)) * xes;
-    const uintptr_t xb = reinterpret_cast<uintptr_t>(x), rb = reinterpret_cast<uintptr_t>(residual);
-    AVEY_REQUIRE(o + on <= xb || xb + xn <= o, AVEY_ERR_INVALID_ARG, "%s: out overlaps x", fn);
-    const uintptr_t rn = (n * ld_res + p->N) * 4;
-    AVEY_REQUIRE(!residual || (rb == o && (ld_res == ld_out || rows == 1)) || o + on <= rb || rb + rn <= o,
-                 AVEY_ERR_INVALID_ARG,
-                 "%s: out overlaps the residual without being it", fn);
+    const uint64_t n = rows, N = p->N, K = p->K;
+    const uint64_t oes = out_dt == AVEY_F32 ? 4 : 2, xes = x_dt == AVEY_I8 ? 1 : x_dt == AVEY_F32 ? 4 : 2;
+    const ByteRows o{reinterpret_cast<uintptr_t>(out), out_dt == AVEY_BF16X2 ? 2 * n : n, N * oes, ld_out * oes};
+    const ByteRows xr{reinterpret_cast<uintptr_t>(x), x_dt == AVEY_BF16X2 ? 2 * n : n, K * xes, ld_x * xes};
+    const ByteRows r{reinterpret_cast<uintptr_t>(residual), n, N * 4, static_cast<uint64_t>(ld_res) * 4};
+    AVEY_REQUIRE(!rows_overlap(o, xr), AVEY_ERR_INVALID_ARG, "%s: out overlaps x", fn);
+    AVEY_REQUIRE(!residual || (r.at == o.at && (ld_res == ld_out || rows == 1)) || !rows_overlap(o, r),
+                 AVEY_ERR_INVALID_ARG, "%s: out overlaps the residual without being it", fn);
   }
   const size_t need = avey_linear_i8_workspace_bytes(x_dt, rows, p->K);
   AVEY_REQUIRE(need == 0 || (ws && (reinterpret_cast<uintptr_t>(ws) & 255) == 0), AVEY_ERR_INVALID_ARG,

@@ -940,11 +940,10 @@ extern "C" avey_status avey_token_logprobs_backward(const void *logits, avey_dty
                    aligned8(stats) && aligned4(entropy) && aligned4(d_logprob) && aligned4(d_entropy),
                AVEY_ERR_INVALID_ARG, "%s: dlogits aligned to its element, stats 8-byte, rows 4-byte", fn);
   {
-    const uintptr_t es = dt == AVEY_F32 ? 4 : 2;
-    const uintptr_t x0 = reinterpret_cast<uintptr_t>(logits), d0 = reinterpret_cast<uintptr_t>(dlogits);
-    const uintptr_t xn = x0 + (static_cast<uintptr_t>(rows - 1) * ld + V) * es;
-    const uintptr_t dn = d0 + (static_cast<uintptr_t>(rows - 1) * ld_d + V) * es;
-    AVEY_REQUIRE((x0 == d0 && ld == ld_d) || dn <= x0 || xn <= d0, AVEY_ERR_INVALID_ARG,
+    const uint64_t n = rows, es = dt == AVEY_F32 ? 4 : 2;
+    const ByteRows x{reinterpret_cast<uintptr_t>(logits), n, V * es, ld * es};
+    const ByteRows d{reinterpret_cast<uintptr_t>(dlogits), n, V * es, ld_d * es};
+    AVEY_REQUIRE((x.at == d.at && ld == ld_d) || !rows_overlap(x, d), AVEY_ERR_INVALID_ARG,
                  "%s: dlogits overlaps the logits without being them", fn);
   }
   LpGradArgs a{};

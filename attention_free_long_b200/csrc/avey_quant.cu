@@ -163,11 +163,11 @@ extern "C" avey_status avey_quantize_rows(const void *x, avey_dtype dt, int rows
   AVEY_REQUIRE(aligned16(q) && (reinterpret_cast<uintptr_t>(scale) & 3) == 0, AVEY_ERR_INVALID_ARG,
                "avey_quantize_rows: q 16-byte and scale 4-byte aligned");
   {
-    const uintptr_t n = static_cast<uintptr_t>(rows - 1), es = dt == AVEY_F32 ? 4 : 2;
-    const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), q0 = reinterpret_cast<uintptr_t>(q);
-    const uintptr_t xn = x0 + (n * ld_x + cols + (dt == AVEY_BF16X2 ? rows * ld_x : 0)) * es;
-    const uintptr_t qn = q0 + n * ld_q + (cols + 15) / 16 * 16;  // with the zeros behind its last row
-    AVEY_REQUIRE(xn <= q0 || qn <= x0, AVEY_ERR_INVALID_ARG, "avey_quantize_rows: q overlaps x");
+    const uint64_t n = rows, es = dt == AVEY_F32 ? 4 : 2;
+    const ByteRows xr{reinterpret_cast<uintptr_t>(x), dt == AVEY_BF16X2 ? 2 * n : n, cols * es, ld_x * es};
+    // with the zeros behind the columns
+    const ByteRows qr{reinterpret_cast<uintptr_t>(q), n, (cols + 15ull) / 16 * 16, static_cast<uint64_t>(ld_q)};
+    AVEY_REQUIRE(!rows_overlap(xr, qr), AVEY_ERR_INVALID_ARG, "avey_quantize_rows: q overlaps x");
   }
   return launch_quantize_rows(x, dt, rows, cols, ld_x, prenorm ? 1 : 0, q, ld_q, scale,
                               reinterpret_cast<cudaStream_t>(stream));
