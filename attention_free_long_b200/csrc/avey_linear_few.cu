@@ -85,6 +85,7 @@ __device__ __forceinline__ void quantize_row_to(const FewArgs &a, int row, int8_
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
   const RowScale rs(mx, false);
+  const bool again = a.prenorm && squares_overflow(ss, mx);
   if (lane == 0)
     *scale = a.prenorm ? rs.scale * (1.0f / sqrtf(ss / static_cast<float>(a.K) + 1e-6f)) : rs.scale;
 #pragma unroll
@@ -94,6 +95,10 @@ __device__ __forceinline__ void quantize_row_to(const FewArgs &a, int row, int8_
     QuantRaw<DT> t;
     src.load(g, t);
     *reinterpret_cast<uint2 *>(dst + g * 8) = rs.quantize8(t);
+  }
+  if (again) {
+    const float sc = shrunk_scale<DT, 32>(a.x, row, a.rows, a.K, a.ld_x, lane);
+    if (lane == 0) *scale = sc;
   }
 }
 

@@ -16,9 +16,10 @@ namespace {
 
 constexpr int kGroups = 4;  // groups of 8 values a thread keeps in registers
 
-// LPR threads per row: as few as hold it.
+// LPR threads per row: as few as hold it.  The normalised forms are held to 64
+// registers: the call behind the rounding would raise them to 72, three blocks an SM.
 template <int DT, int LPR, bool PRENORM, bool FAST>
-__global__ void __launch_bounds__(256) quantize_rows(const void *__restrict__ x, int rows, int cols,
+__global__ void __launch_bounds__(256, PRENORM ? 4 : 0) quantize_rows(const void *__restrict__ x, int rows, int cols,
                                                      long long ld_x, int8_t *__restrict__ q,
                                                      long long ld_q, float *__restrict__ scale) {
   constexpr int RPB = 256 / LPR, WPR = LPR / 32;  // rows per block, warps per row
@@ -74,6 +75,8 @@ __global__ void __launch_bounds__(256) quantize_rows(const void *__restrict__ x,
   const RowScale rs(mx, DT == AVEY_BF16);
   if (me == 0)
     scale[row] = PRENORM ? rs.scale * (1.0f / sqrtf(ss / static_cast<float>(cols) + 1e-6f)) : rs.scale;
+  constexpr int L = LPR < 32 ? LPR : 32;
+  const bool again = PRENORM && me < L && squares_overflow(ss, mx);
   int8_t *qr = q + row * ld_q;
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
@@ -84,6 +87,12 @@ __global__ void __launch_bounds__(256) quantize_rows(const void *__restrict__ x,
     QuantRaw<DT> t;
     src.load(g, t);
     *reinterpret_cast<uint2 *>(qr + g * 8ll) = rs.quantize8(t);
+  }
+  if (again) {
+    const int lane0 = threadIdx.x % LPR;
+    const long long r = static_cast<long long>(blockIdx.x) * RPB + threadIdx.x / LPR;
+    const float sc = shrunk_scale<DT, L>(x, r, rows, cols, ld_x, lane0);
+    if (lane0 == 0) scale[r] = sc;
   }
 }
 

@@ -138,6 +138,43 @@ struct QuantScan {
   __device__ __forceinline__ float squares() const { return ss.x + ss.y; }
 };
 
+// Squares of finite values may leave fp32 (from |x| = 1.8e19 on), which would leave
+// the scale s / sqrt(mean(x^2)) at 0.
+__device__ __forceinline__ bool squares_overflow(float ss, uint32_t max_bits) {
+  return ss == INFINITY && max_bits < 0x7f800000u;
+}
+// The normalised scale of such a row, by L lanes of one warp, of which this is number
+// `me`: the squares are those of the values times 2^-96, where none overflows, what is
+// lost below is nothing to their sum, and 1e-6 is far below an ulp of the mean.  A
+// function apart that reads the row again, so that the rows that do not need it pay
+// no registers for it.
+template <int DT, int L>
+__device__ __noinline__ float shrunk_scale(const void *x, long long row, long long rows, int cols, long long ld,
+                                           int me) {
+  constexpr float kShrink = 0x1p-96f;
+  const QuantSource<DT, false> src(x, row, rows, cols, ld);
+  float ss = 0.f, mx = 0.f;
+#pragma unroll 1
+  for (int g = me; g < (cols + 7) / 8; g += L) {
+    QuantRaw<DT> r;
+    float v[8];
+    src.load(g, r);
+    r.values(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      mx = fmaxf(mx, fabsf(v[i]));
+      ss = fmaf(v[i] * kShrink, v[i] * kShrink, ss);
+    }
+  }
+  const uint32_t lanes = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1u) << ((threadIdx.x & 31) - me);
+#pragma unroll
+  for (int off = L / 2; off > 0; off >>= 1) {
+    ss += __shfl_xor_sync(lanes, ss, off);
+    mx = fmaxf(mx, __shfl_xor_sync(lanes, mx, off));
+  }
+  return __fmul_rn(mx, 1.0f / 127.0f) * kShrink * (1.0f / sqrtf(ss / static_cast<float>(cols)));
+}
+
 // The scale of a row from the bits of its largest magnitude, and the rounding.
 struct RowScale {
   float scale;  // s; NaN for a row that is not finite
