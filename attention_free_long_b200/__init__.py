@@ -586,7 +586,9 @@ def avey_token_logprobs_backward(logits: torch.Tensor, ids: Optional[torch.Tenso
                                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of sum(d_logprob * logprob) + sum(d_entropy * entropy) with
     respect to the logits; scores: what avey_token_logprobs gave for them.
-    out may be the logits."""
+    out may be the logits.  Rows that lie as the logits' modulo 16 bytes are
+    written fastest: for padded logits (avey_linear_i8's where N % 8) give an out
+    of their row stride, or the logits."""
     rows, V, ld = _rows_of(logits, "logits")
     dt = _dt(logits)
     _vector(ids, "ids", rows, torch.int32)

@@ -399,8 +399,9 @@ AVEY_API avey_status avey_quantize_rows(const void *x, avey_dtype dt, int rows, 
  * Constraints: rows >= 0 (0: nothing is done), K, N >= 1, K <= 131071 (the
  * int32 sum); ld_w % 16 == 0, ld_x % 16 == 0 for AVEY_I8, ld_out % 8 == 0;
  * ld_res >= N; Wq, w_scale, bias, out and AVEY_I8 x 16-byte aligned.  out must not
- * overlap x, nor the residual unless it is the residual (both are checked), nor
- * any other buffer of the call.
+ * overlap x, nor the residual unless it is the residual (both are checked: operands
+ * that are other columns of one buffer, rows of one stride, share nothing), nor any
+ * other buffer of the call.
  */
 enum { AVEY_ACT_NONE = 0, AVEY_ACT_RELU2 = 1 };
 
@@ -456,9 +457,12 @@ AVEY_API avey_status avey_token_logprobs(const void *logits, avey_dtype dt, int 
  * logits, ids, stats and entropy as given to and written by
  * avey_token_logprobs.  d_logprob (with ids) or d_entropy (with entropy) may be
  * NULL for 0.  A row with g = h = 0 gets zeros whatever its logits hold, a row
- * of -inf alone too; -inf entries get 0.
+ * of -inf alone too; -inf entries get 0, but for the given token: p is 0 there and
+ * the formula leaves g.
  * dlogits [rows, V], type of the logits, leading dimension ld_d; may be the
- *         logits themselves (same ld), no partial overlap.
+ *         logits themselves (same ld), no partial overlap.  Written in 16-byte
+ *         words where its rows lie as the logits' modulo 16 bytes, by value
+ *         elsewhere.
  * Constraints as avey_token_logprobs.
  */
 AVEY_API avey_status avey_token_logprobs_backward(const void *logits, avey_dtype dt, int rows, int V,
