@@ -14,6 +14,7 @@
 // channels as the rows of a tile 13.5, two launches.  More rows or longer ones mean
 // more to prepare per block: from 9 rows on only up to K = 768 (12 rows against
 // 65536 x 1024: 19.4 and 17.4 us; 40000 x 2048: 27.5 and 21.7), and none from 17.
+// Up to 8 rows fit up to K = 12160, 96 KB of tokens.
 // Scored (1 x 768 -> 50368: 12.7 us, with the logits in memory 14.9) a block leaves the
 // softmax statistics of its channels, and a block per token joins them.
 #include <algorithm>

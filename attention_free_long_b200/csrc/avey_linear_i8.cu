@@ -1112,8 +1112,11 @@ avey_status launch_score_i8(const avey_linear_i8_params *p, const int8_t *xq, in
 }  // namespace
 }  // namespace avey
 
-// Up to this many rows the logits go through the workspace (32 x 768 -> 50368: 19.3 us
-// so, 21.2 with the statistics in the product; 17 x 256: 14.5 and 18.3).
+// Scores take the few-row kernel where it fits (linear_few_fits).  Else up to 16 rows
+// send their logits through the workspace, and up to this many where channels become
+// the rows of a tile (swap_pays; 32 x 768 -> 50368: 19.3 us so, 21.2 with the
+// statistics in the product; 17 x 256: 14.5 and 18.3).  All others keep the statistics
+// in the product.
 static constexpr int kLogitRows = 32;
 
 extern "C" size_t avey_score_tokens_i8_workspace_bytes(int rows, int K, int N) {
